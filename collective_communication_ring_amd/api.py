@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libar.so")
 
 # ---- constants mirrored from include/ar.h --------------------------------
-AR_INT32, AR_FLOAT32, AR_BF16 = 0, 1, 2
+AR_INT32, AR_FLOAT32, AR_BF16, AR_E4M3 = 0, 1, 2, 3
 AR_RING, AR_TREE, AR_AUTO = 0, 1, 2
 AR_SIMPLE, AR_LL, AR_PROTO_AUTO = 0, 1, 2
 AR_SUCCESS, AR_ERR_INVALID_ARG, AR_ERR_INVALID_USAGE, AR_ERR_UNSUPPORTED = 0, 1, 2, 3
@@ -40,6 +40,34 @@ LAUNCHES = {"auto": AR_LAUNCH_AUTO, "step": AR_LAUNCH_STEP, "fused": AR_LAUNCH_F
 ELEM_SIZE = {AR_INT32: 4, AR_FLOAT32: 4, AR_BF16: 2}
 
 _lib = None
+
+
+class ar_span_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("count", ctypes.c_size_t), ("dtype", ctypes.c_int)]
+
+
+class ar_rmsnorm_t(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("rows", ctypes.c_size_t), ("cols", ctypes.c_size_t), ("group", ctypes.c_size_t),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_size_t),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_size_t),
+                ("weight", ctypes.c_void_p),
+                ("sum", ctypes.c_void_p), ("sum_stride", ctypes.c_size_t),
+                ("y", ctypes.c_void_p), ("y_stride", ctypes.c_size_t),
+                ("scale", ctypes.c_void_p), ("rstd", ctypes.c_void_p)]
+
+
+class ar_rmsnorm_backward_t(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("ranks", ctypes.c_int),
+                ("rows", ctypes.c_size_t), ("cols", ctypes.c_size_t),
+                ("dy", ctypes.c_void_p), ("dy_stride", ctypes.c_size_t),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_size_t),
+                ("weight", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("dsum", ctypes.c_void_p), ("dsum_stride", ctypes.c_size_t),
+                ("dx", ctypes.c_void_p), ("dx_stride", ctypes.c_size_t),
+                ("dweight", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class ArError(RuntimeError):
@@ -85,6 +113,13 @@ def lib():
         "ar_stream_create_cu_masked": ([ctypes.POINTER(vp), ctypes.c_uint32,
                                         ctypes.POINTER(ctypes.c_uint32)], i),
         "ar_stream_destroy": ([vp], i),
+        "ar_rmsnorm": ([ctypes.POINTER(ar_rmsnorm_t), vp], i),
+        "ar_reduce_scatter_rmsnorm": ([vp, vp, ctypes.POINTER(ar_rmsnorm_t), vp], i),
+        "ar_rmsnorm_backward": ([ctypes.POINTER(ar_rmsnorm_backward_t), vp], i),
+        "ar_rmsnorm_backward_workspace": ([i, sz, sz], sz),
+        "ar_grad_norm": ([vp, ctypes.POINTER(ar_span_t), sz, vp, vp], i),
+        "ar_grad_clip": ([ctypes.POINTER(ar_span_t), ctypes.POINTER(ar_span_t), sz, vp,
+                          ctypes.c_float, vp], i),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -229,11 +264,237 @@ def ar_stream_destroy(stream):
     _ok(lib().ar_stream_destroy(stream), "ar_stream_destroy")
 
 
+def ar_rmsnorm(args, stream=0):
+    """args: an ar_rmsnorm_t."""
+    _ok(lib().ar_rmsnorm(args, stream), "ar_rmsnorm")
+
+
+def ar_reduce_scatter_rmsnorm(comm, send_ptr, args, stream=0):
+    _ok(lib().ar_reduce_scatter_rmsnorm(comm, send_ptr, args, stream), "ar_reduce_scatter_rmsnorm")
+
+
+def ar_rmsnorm_backward(args, stream=0):
+    """args: an ar_rmsnorm_backward_t."""
+    _ok(lib().ar_rmsnorm_backward(args, stream), "ar_rmsnorm_backward")
+
+
+def ar_rmsnorm_backward_workspace(ranks, rows, cols):
+    """Bytes; 0 for sizes that ar_rmsnorm_backward refuses."""
+    return lib().ar_rmsnorm_backward_workspace(ranks, rows, cols)
+
+
+def ar_grad_norm(comm, spans, n, norm_ptr, stream=0):
+    """spans: a ctypes array of ar_span_t."""
+    _ok(lib().ar_grad_norm(comm, spans, n, norm_ptr, stream), "ar_grad_norm")
+
+
+def ar_grad_clip(spans, out_spans, n, norm_ptr, max_norm, stream=0):
+    _ok(lib().ar_grad_clip(spans, out_spans, n, norm_ptr, max_norm, stream), "ar_grad_clip")
+
+
 # ---- torch convenience wrapper ---------------------------------------------
 
 def _torch_dtype(dt):
     import torch
     return {AR_INT32: torch.int32, AR_FLOAT32: torch.float32, AR_BF16: torch.bfloat16}[dt]
+
+
+def _dtype_code(dtype):
+    """AR_* of a torch dtype's name (None: not one of the library's)."""
+    return {"torch.int32": AR_INT32, "torch.float32": AR_FLOAT32, "torch.bfloat16": AR_BF16,
+            "torch.float8_e4m3fn": AR_E4M3}.get(str(dtype))
+
+
+def _raw_stream(device, stream):
+    import torch
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+def _check_stream_types(x, weight, what):
+    """AR_* codes of a norm's stream and weight tensors."""
+    dt = _dtype_code(x.dtype)
+    if dt not in (AR_FLOAT32, AR_BF16):
+        raise ValueError("%s has dtype %s: float32 or bfloat16 is wanted" % (what, x.dtype))
+    wdt = _dtype_code(weight.dtype)
+    if wdt != dt and wdt != AR_FLOAT32:
+        raise ValueError("weight has dtype %s: %s or torch.float32 is wanted"
+                         % (weight.dtype, x.dtype))
+    if weight.dim() != 1 or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous vector")
+    return dt, wdt
+
+
+def _check_like(t, device, shape, dtype, what, contiguous=False):
+    """A tensor of this device, shape and dtype whose last dimension is
+    contiguous (or all of it); returns its address, None for None."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError("%s must be on %s, not %s" % (what, device, t.device))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s has dtype %s, not %s" % (what, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, not %s" % (what, tuple(shape), tuple(t.shape)))
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % what)
+    elif t.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError("the last dimension of %s must be contiguous" % what)
+    return t.data_ptr()
+
+
+def _check_norm_outputs(x, y, scale, group, rows, cols, dtype):
+    """Output code of a norm, its groups per row, and scale's expected presence."""
+    out = _dtype_code(y.dtype)
+    if out != dtype and out != AR_E4M3:
+        raise ValueError("y has dtype %s: %s or torch.float8_e4m3fn is wanted" % (y.dtype, x.dtype))
+    if out != AR_E4M3:
+        if scale is not None or group:
+            raise ValueError("scale and group belong to an e4m3 output")
+        return out, 0
+    if scale is None:
+        raise ValueError("an e4m3 output needs scale")
+    if group not in (0, 32, 64, 128, 256):
+        raise ValueError("group must be 0 (a whole row), 32, 64, 128 or 256, got %r" % (group,))
+    return out, -(-cols // group) if group else 1
+
+
+def rmsnorm(x, weight, y, eps=1e-6, residual=None, sum=None, scale=None, group=0, rstd=None,
+            stream=None):
+    """RMS norm of x + residual (``ar_rmsnorm``): y = h / sqrt(mean(h^2) + eps)
+    * weight with h = x + residual, written to ``y``; h to ``sum`` and
+    1 / sqrt(mean(h^2) + eps) to ``rstd`` [rows] where given.
+
+    x, residual, sum: [rows, cols] of float32 or bfloat16, rows any distance
+    apart; y the same, or float8_e4m3fn with ``scale`` [rows, ceil(cols /
+    group)] float32, one scale for each ``group`` (32, 64, 128, 256; 0: all)
+    columns.  sum or y may be x or residual.  Asynchronous on the current
+    torch stream (or the given one)."""
+    if x.dim() != 2:
+        raise ValueError("x must have shape (rows, cols), got %s" % (tuple(x.shape),))
+    shape = x.shape
+    rows, cols = shape
+    dt, wdt = _check_stream_types(x, weight, "x")
+    out, groups = _check_norm_outputs(x, y, scale, group, rows, cols, dt)
+    dev = x.device
+    if not x.is_cuda:
+        raise ValueError("x must be on the GPU")
+    import torch
+    f32 = torch.float32
+    args = ar_rmsnorm_t(
+        dt, out, wdt, eps, rows, cols, group,
+        _check_like(x, dev, shape, None, "x"), x.stride(0),
+        _check_like(residual, dev, shape, x.dtype, "residual"),
+        residual.stride(0) if residual is not None else 0,
+        _check_like(weight, dev, shape[1:], None, "weight"),
+        _check_like(sum, dev, shape, x.dtype, "sum"), sum.stride(0) if sum is not None else 0,
+        _check_like(y, dev, shape, None, "y"), y.stride(0),
+        _check_like(scale, dev, (rows, groups), f32, "scale", True),
+        _check_like(rstd, dev, shape[:1], f32, "rstd", True))
+    ar_rmsnorm(args, _raw_stream(dev, stream))
+    return y
+
+
+def rmsnorm_backward_workspace(ranks, rows, cols, device="cuda"):
+    """A workspace for ``rmsnorm_backward`` calls of these sizes (a tensor the
+    caller keeps; one call at a time may use it)."""
+    import torch
+    return torch.empty(max(256, ar_rmsnorm_backward_workspace(ranks, rows, cols)),
+                       dtype=torch.uint8, device=device)
+
+
+def rmsnorm_backward(dy, x, weight, rstd, dx, dweight, dsum=None, workspace=None, stream=None):
+    """Backward pass of ``rmsnorm`` (``ar_rmsnorm_backward``): dx [rows, cols]
+    is the gradient of x + residual (x here is the forward's ``sum``, or its x
+    where it had no residual), plus ``dsum``, the gradient that reaches the
+    sum from elsewhere; dweight is [ranks, cols] float32, a row for each of
+    ``ranks`` equal shards of the rows.  dx may be dy, x or dsum.  Without
+    ``workspace`` (``rmsnorm_backward_workspace``) one is allocated."""
+    if x.dim() != 2 or dweight.dim() != 2:
+        raise ValueError("x must have shape (rows, cols) and dweight (ranks, cols)")
+    import torch
+    shape = x.shape
+    rows, cols = shape
+    ranks = dweight.shape[0]
+    dt, wdt = _check_stream_types(x, weight, "x")
+    dev = x.device
+    if not x.is_cuda:
+        raise ValueError("x must be on the GPU")
+    if ranks < 1 or rows % ranks:
+        raise ValueError("%d rows are not %d equal shards" % (rows, ranks))
+    if workspace is None:
+        workspace = rmsnorm_backward_workspace(ranks, rows, cols, dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+    f32 = torch.float32
+    args = ar_rmsnorm_backward_t(
+        dt, wdt, ranks, rows, cols,
+        _check_like(dy, dev, shape, x.dtype, "dy"), dy.stride(0),
+        _check_like(x, dev, shape, None, "x"), x.stride(0),
+        _check_like(weight, dev, shape[1:], None, "weight"),
+        _check_like(rstd, dev, shape[:1], f32, "rstd", True),
+        _check_like(dsum, dev, shape, x.dtype, "dsum"), dsum.stride(0) if dsum is not None else 0,
+        _check_like(dx, dev, shape, x.dtype, "dx"), dx.stride(0),
+        _check_like(dweight, dev, (ranks, cols), f32, "dweight", True),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ar_rmsnorm_backward(args, _raw_stream(dev, stream))
+    return dx
+
+
+def _dense(t):
+    """Whether a tensor's elements fill one block of memory, in any order of
+    its dimensions."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size == 1:
+            continue
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+class TensorList:
+    """Gradient tensors of one GPU as ``Comm.grad_norm`` / ``Comm.grad_clip``
+    take them: float32 or bfloat16, each dense in memory.  Keeps the tensors,
+    and their addresses in a form that a call need not build again; an address
+    that has changed (``t.data`` was set) is taken up by the next call."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.device = self.tensors[0].device if self.tensors else None
+        self._array = (ar_span_t * len(self.tensors))()
+        self._fill()
+
+    def _fill(self):
+        for i, t in enumerate(self.tensors):
+            dt = _dtype_code(t.dtype)
+            if dt not in (AR_FLOAT32, AR_BF16):
+                raise ValueError("tensor %d has dtype %s: float32 or bfloat16 is wanted" % (i, t.dtype))
+            if t.device != self.device or not t.is_cuda:
+                raise ValueError("tensor %d is on %s: all must be on one GPU" % (i, t.device))
+            if not _dense(t):
+                raise ValueError("tensor %d is not dense in memory" % i)
+            self._array[i] = ar_span_t(t.data_ptr(), t.numel(), dt)
+        self._ptrs = [t.data_ptr() for t in self.tensors]
+        # element for element: an output needs its input's type and layout
+        self._layout = [(t.dtype, t.shape, t.stride()) for t in self.tensors]
+
+    def __len__(self):
+        return len(self.tensors)
+
+    def spans(self):
+        if [t.data_ptr() for t in self.tensors] != self._ptrs:
+            self._fill()
+        return self._array
+
+
+def _tensor_list(tensors):
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
 
 
 class Comm:
@@ -305,6 +566,64 @@ class Comm:
         self._check_tensor(recv, self.R, n * self.R, "recv")
         ar_all_gather(self.handle, send.data_ptr(), recv.data_ptr(), n, self._stream(stream))
         return recv
+
+    def reduce_scatter_rmsnorm(self, send, weight, y, eps=1e-6, residual=None, sum=None,
+                               scale=None, group=0, rstd=None, stream=None):
+        """Reduce-scatter of ``send`` [R, R * tokens * cols] with an RMS norm
+        behind it, in one pass (``ar_reduce_scatter_rmsnorm``).  Rank q's row
+        of residual, sum and y ([R, tokens * cols]) holds its own tokens;
+        weight [cols] gives the row length; rstd is [R, tokens] and scale
+        [R, tokens * ceil(cols / group)].  Otherwise as ``rmsnorm``."""
+        import torch
+        cols = weight.shape[0] if weight.dim() == 1 else 0
+        if y.dim() != 2 or y.shape[0] != self.R or (cols and y.shape[1] % cols):
+            raise ValueError("y must have shape (%d, tokens * %d), got %s"
+                             % (self.R, cols, tuple(y.shape)))
+        n = y.shape[1]
+        tokens = n // cols if cols else 0
+        self._check_tensor(send, self.R, n * self.R, "send")
+        dt, wdt = _check_stream_types(send, weight, "send")
+        out, groups = _check_norm_outputs(send, y, scale, group, tokens, cols, dt)
+        dev, shape, f32 = send.device, (self.R, n), torch.float32
+        args = ar_rmsnorm_t(
+            dt, out, wdt, eps, tokens, cols, group, None, 0,
+            _check_like(residual, dev, shape, send.dtype, "residual", True), 0,
+            _check_like(weight, dev, (cols,), None, "weight"),
+            _check_like(sum, dev, shape, send.dtype, "sum", True), 0,
+            _check_like(y, dev, shape, None, "y", True), 0,
+            _check_like(scale, dev, (self.R, tokens * groups), f32, "scale", True),
+            _check_like(rstd, dev, (self.R, tokens), f32, "rstd", True))
+        ar_reduce_scatter_rmsnorm(self.handle, send.data_ptr(), args, self._stream(stream))
+        return y
+
+    def grad_norm(self, grads, norm, stream=None):
+        """Global 2-norm of the tensors of ``grads`` (a sequence, or a
+        ``TensorList`` kept for many calls) to ``norm``, one float32 on the
+        device (``ar_grad_norm``).  Uses the comm's workspace: ordered with its
+        collectives on one stream."""
+        grads = _tensor_list(grads)
+        self._check_norm(grads, norm)
+        ar_grad_norm(self.handle, grads.spans(), len(grads), norm.data_ptr(), self._stream(stream))
+        return norm
+
+    def grad_clip(self, grads, norm, max_norm, out=None, stream=None):
+        """Scales the tensors of ``grads`` to a norm of at most ``max_norm``,
+        ``norm`` being theirs on the device (``ar_grad_clip``): in place, or
+        into the tensors of ``out``."""
+        grads = _tensor_list(grads)
+        out = grads if out is None else _tensor_list(out)
+        self._check_norm(grads, norm)
+        if out is not grads and (out._layout != grads._layout or out.device != grads.device):
+            raise ValueError("out must have the shapes, dtypes, strides and device of grads")
+        ar_grad_clip(grads.spans(), grads.spans() if out is grads else out.spans(), len(grads),
+                     norm.data_ptr(), max_norm, self._stream(stream))
+        return norm
+
+    def _check_norm(self, grads, norm):
+        import torch
+        if norm.numel() != 1 or norm.dtype != torch.float32 or not norm.is_cuda or \
+                (grads.device is not None and grads.device != norm.device):
+            raise ValueError("norm must be one float32 on the gradients' device")
 
     def check(self):
         return ar_check(self.handle)

@@ -16,6 +16,7 @@
 
 #include "ar.h"
 #include "ar_internal.h"
+#include "ar_ops.h"
 #include "ar_tree_fused.h"
 
 using namespace ar;
@@ -163,6 +164,7 @@ struct ar_comm {
     uint64_t flag_stride = 0; // pipelined ring: ready flags per segment
     size_t off_rll = 0;       // ring-LL line slots
     uint64_t rll_cap = 0;     // ring-LL: lines per (sender, segment) per launch
+    size_t off_norm = 0;      // gradient norm: partial sums of kGradMaxBlocks workgroups
     char* ws = nullptr;
     size_t ws_bytes = 0;
     // device facts, read on first use
@@ -886,7 +888,8 @@ int ar_init(ar_comm_t* out, int R, size_t count, ar_dtype_t dtype, ar_algo_t alg
     }
     c->channels = std::min<int64_t>(std::max<int64_t>(1, env_int("AR_CHANNELS", 1)), c->nstrides);
     // workspace: control block | hand-off accumulators [cap] (A) | tree LL up
-    // | down | tree epochs | pipelined flags | ring-LL lines
+    // | down | tree epochs | pipelined flags | ring-LL lines | gradient norm's
+    // partial sums
     const size_t cap1 = count ? count : 1;
     c->tree_lines = std::min<uint64_t>((cap1 + 1) / 2, kTreeLinesCap);
     size_t off = kAlign;  // control block
@@ -915,6 +918,8 @@ int ar_init(ar_comm_t* out, int R, size_t count, ar_dtype_t dtype, ar_algo_t alg
     c->rll_cap = std::min<uint64_t>((cap1 + R - 1) / R,
                                     std::max<uint64_t>(64, (uint64_t)(1u << 21) / ((uint64_t)R * R)));
     off = align_up(off + (size_t)R * R * c->rll_cap * 8, kAlign);
+    c->off_norm = off;
+    off = align_up(off + (size_t)kGradMaxBlocks * sizeof(double), kAlign);
     c->ws_need = off;
     *out = c;
     return AR_SUCCESS;
@@ -1112,6 +1117,50 @@ int ar_all_gather(ar_comm_t c, const void* send, void* recv, size_t sendcount, v
     a.op = kOpAllGather;
     a.timeout_ticks = timeout_ticks(c);
     return run_ring(c, a, st, ws_opts(c, N));
+}
+
+int ar_reduce_scatter_rmsnorm(ar_comm_t c, const void* send, const ar_rmsnorm_t* args, void* stream)
+{
+    if (!c || !args)
+        return AR_ERR_INVALID_ARG;
+    if (c->dtype == AR_INT32 || c->algo == AR_TREE || (c->redop != AR_SUM && c->redop != AR_AVG))
+        return AR_ERR_UNSUPPORTED;
+    ar_rmsnorm_t p = *args;
+    // sizes first, by division, so that no product wraps around
+    const size_t most = c->cap / (size_t)c->R;  // elements of one rank's tokens
+    if (p.cols && p.rows > most / p.cols)
+        return AR_ERR_INVALID_ARG;
+    p.dtype = c->dtype;
+    p.rows *= (size_t)c->R;
+    p.x = send;
+    p.x_stride = p.residual_stride = p.sum_stride = p.y_stride = p.cols;
+    NormArgs a{};
+    bool noop = false;
+    const int rc = norm_prepare(p, c->R, &a, &noop);
+    if (rc || noop)
+        return rc;
+    a.divisor = c->redop == AR_AVG ? (float)c->R : 1.0f;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    c->last_stream = st;
+    const hipError_t e = launch_rmsnorm(c->dtype, p.out_dtype == AR_E4M3, a, st);
+    return e == hipSuccess ? AR_SUCCESS : fail_hip(c, e);
+}
+
+int ar_grad_norm(ar_comm_t c, const ar_span_t* grads, size_t n, float* norm, void* stream)
+{
+    if (!c)
+        return AR_ERR_INVALID_ARG;
+    if (!c->ws)
+        return AR_ERR_INVALID_USAGE;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = hipSuccess;
+    const int rc = grad_norm_run(grads, n, norm, reinterpret_cast<double*>(c->ws + c->off_norm),
+                                 reinterpret_cast<uint32_t*>(c->ws) + kCtrlNormTicket, st, &e);
+    if (rc == AR_ERR_HIP)
+        return fail_hip(c, e);
+    if (rc == AR_SUCCESS)
+        c->last_stream = st;
+    return rc;
 }
 
 int ar_check(ar_comm_t c)

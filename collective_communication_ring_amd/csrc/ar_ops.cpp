@@ -1,0 +1,384 @@
+// ar_ops.cpp -- host side of the operators around the collectives: argument
+// checks, workspace sizes, and the tables of gradient lists.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "ar_internal.h"
+#include "ar_ops.h"
+
+using namespace ar;
+
+namespace {
+
+constexpr size_t kMaxElems = (size_t)1 << 46;  // sizes above are refused: no byte offset wraps
+
+size_t size_of(int dtype) { return dtype == AR_E4M3 ? 1 : dtype == AR_BF16 ? 2 : 4; }
+
+bool stream_type(int dtype) { return dtype == AR_FLOAT32 || dtype == AR_BF16; }
+
+bool misaligned(const void* p, int dtype) { return (uintptr_t)p % size_of(dtype) != 0; }
+
+// An array of `rows` rows of `len` bytes, `stride` bytes apart.
+struct Rows {
+    uintptr_t at;
+    uint64_t rows, len, stride;
+};
+
+Rows rows_of(const void* p, size_t rows, size_t cols, size_t stride, int dtype)
+{
+    const size_t z = size_of(dtype);
+    return {(uintptr_t)p, rows, cols * z, stride * z};
+}
+
+// Whether two arrays share a byte (a NULL one shares none).  Rows of one
+// stride may lie between each other's; with two strides the extents decide.
+bool share(const Rows& a, const Rows& b)
+{
+    if (!a.at || !b.at || !a.rows || !b.rows)
+        return false;
+    if (a.at + (a.rows - 1) * a.stride + a.len <= b.at || b.at + (b.rows - 1) * b.stride + b.len <= a.at)
+        return false;
+    const uint64_t stride = a.rows > 1 ? a.stride : b.stride;
+    if ((a.rows == 1 && b.rows == 1) || (a.rows > 1 && b.rows > 1 && a.stride != b.stride))
+        return true;
+    const uint64_t d = b.at >= a.at ? (b.at - a.at) % stride
+                                    : (stride - (a.at - b.at) % stride) % stride;
+    return d < a.len || d + b.len > stride;
+}
+
+// The same rows in the same type: an output may replace this input.
+bool same(const Rows& a, const Rows& b)
+{
+    return a.at == b.at && a.len == b.len && (a.rows == 1 || a.stride == b.stride);
+}
+
+// Outputs against each other and against the inputs.  in[0 .. in_place) may be
+// an output's array.
+bool disjoint(const Rows* out, int nout, const Rows* in, int nin, int in_place)
+{
+    for (int i = 0; i < nout; ++i) {
+        for (int j = i + 1; j < nout; ++j)
+            if (share(out[i], out[j]))
+                return false;
+        for (int j = 0; j < nin; ++j)
+            if (share(out[i], in[j]) && !(j < in_place && same(out[i], in[j])))
+                return false;
+    }
+    return true;
+}
+
+// Rows of `cols` elements `*stride` apart: the stride of a single row means
+// nothing, else rows must not overlap and the array stay below kMaxElems.
+bool bad_stride(size_t rows, size_t cols, size_t* stride)
+{
+    if (rows == 1)
+        *stride = cols;
+    return *stride < cols || *stride > kMaxElems / rows;
+}
+
+int done(hipError_t e)
+{
+    if (e == hipSuccess)
+        return AR_SUCCESS;
+    g_util_hip_error = (int)e;
+    return AR_ERR_HIP;
+}
+
+}  // namespace
+
+namespace ar {
+
+int norm_prepare(ar_rmsnorm_t p, int parts, NormArgs* out, bool* noop)
+{
+    *noop = false;
+    if (!stream_type(p.dtype) || (p.out_dtype != p.dtype && p.out_dtype != AR_E4M3) ||
+        (p.weight_dtype != p.dtype && p.weight_dtype != AR_FLOAT32))
+        return AR_ERR_INVALID_ARG;
+    if (!(p.eps >= 0.0f) || std::isinf(p.eps) || p.cols > kNormMaxCols || p.rows > kMaxElems)
+        return AR_ERR_INVALID_ARG;
+    const bool e4m3 = p.out_dtype == AR_E4M3;
+    if (e4m3 && p.group != 0 && p.group != 32 && p.group != 64 && p.group != 128 && p.group != 256)
+        return AR_ERR_INVALID_ARG;
+    if (p.rows == 0 || p.cols == 0) {
+        *noop = true;
+        return AR_SUCCESS;
+    }
+    if (!p.x || !p.weight || !p.y || (e4m3 && !p.scale))
+        return AR_ERR_INVALID_ARG;
+    if (bad_stride(p.rows, p.cols, &p.x_stride) || bad_stride(p.rows, p.cols, &p.y_stride) ||
+        (p.residual && bad_stride(p.rows, p.cols, &p.residual_stride)) ||
+        (p.sum && bad_stride(p.rows, p.cols, &p.sum_stride)))
+        return AR_ERR_INVALID_ARG;
+    if (misaligned(p.x, p.dtype) || misaligned(p.residual, p.dtype) || misaligned(p.sum, p.dtype) ||
+        misaligned(p.y, p.out_dtype) || misaligned(p.weight, p.weight_dtype) ||
+        misaligned(p.scale, AR_FLOAT32) || misaligned(p.rstd, AR_FLOAT32))
+        return AR_ERR_INVALID_ARG;
+    NormArgs a{};
+    a.x = p.x;
+    a.residual = p.residual;
+    a.weight = p.weight;
+    a.sum = p.sum;
+    a.y = p.y;
+    a.scale = e4m3 ? p.scale : nullptr;
+    a.rstd = p.rstd;
+    a.rows = p.rows;
+    a.x_stride = p.x_stride;
+    a.res_stride = p.residual_stride;
+    a.sum_stride = p.sum_stride;
+    a.y_stride = p.y_stride;
+    a.cols = (uint32_t)p.cols;
+    a.group = e4m3 && p.group && p.group < p.cols ? (uint32_t)p.group : (uint32_t)p.cols;
+    a.groups = (a.cols + a.group - 1) / a.group;
+    a.parts = parts;
+    a.divisor = 1.0f;
+    a.eps = p.eps;
+    a.weight_f32 = p.weight_dtype == AR_FLOAT32;
+    if (parts > 1) {
+        a.part_stride = p.rows * p.cols;
+        a.tokens_per_rank = p.rows / (size_t)parts;
+    }
+    const Rows res = rows_of(p.residual, p.rows, p.cols, p.residual_stride, p.dtype);
+    const Rows x = parts > 1 ? rows_of(p.x, 1, (size_t)parts * p.rows * p.cols, 0, p.dtype)
+                             : rows_of(p.x, p.rows, p.cols, p.x_stride, p.dtype);
+    const Rows w = rows_of(p.weight, 1, p.cols, 0, p.weight_dtype);
+    const Rows outs[] = {rows_of(p.y, p.rows, p.cols, p.y_stride, p.out_dtype),
+                         rows_of(p.sum, p.rows, p.cols, p.sum_stride, p.dtype),
+                         rows_of(a.scale, 1, p.rows * a.groups, 0, AR_FLOAT32),
+                         rows_of(p.rstd, 1, p.rows, 0, AR_FLOAT32)};
+    const Rows ins[] = {res, x, w};
+    if (!disjoint(outs, 4, ins, 3, parts > 1 ? 1 : 2))
+        return AR_ERR_INVALID_USAGE;
+    *out = a;
+    return AR_SUCCESS;
+}
+
+}  // namespace ar
+
+extern "C" int ar_rmsnorm(const ar_rmsnorm_t* args, void* stream)
+{
+    if (!args)
+        return AR_ERR_INVALID_ARG;
+    NormArgs a{};
+    bool noop = false;
+    const int rc = norm_prepare(*args, 1, &a, &noop);
+    if (rc || noop)
+        return rc;
+    return done(launch_rmsnorm(args->dtype, args->out_dtype == AR_E4M3, a,
+                               static_cast<hipStream_t>(stream)));
+}
+
+extern "C" size_t ar_rmsnorm_backward_workspace(int ranks, size_t rows, size_t cols)
+{
+    if (ranks < 1 || ranks > kMaxRanks || rows % (size_t)ranks || cols > kNormMaxCols)
+        return 0;
+    const size_t n = (size_t)ranks * norm_back_blocks(rows / (size_t)ranks, ranks) * cols * 4;
+    return (n + 255) / 256 * 256;
+}
+
+extern "C" int ar_rmsnorm_backward(const ar_rmsnorm_backward_t* args, void* stream)
+{
+    if (!args)
+        return AR_ERR_INVALID_ARG;
+    ar_rmsnorm_backward_t p = *args;
+    if (!stream_type(p.dtype) || (p.weight_dtype != p.dtype && p.weight_dtype != AR_FLOAT32) ||
+        p.ranks < 1 || p.ranks > kMaxRanks || p.rows % (size_t)p.ranks || p.cols > kNormMaxCols ||
+        p.rows > kMaxElems)
+        return AR_ERR_INVALID_ARG;
+    if (p.cols == 0)
+        return AR_SUCCESS;
+    if (!p.dweight || misaligned(p.dweight, AR_FLOAT32))
+        return AR_ERR_INVALID_ARG;
+    if (p.rows) {
+        if (!p.dy || !p.x || !p.weight || !p.rstd || !p.dx || !p.workspace ||
+            p.workspace_bytes < ar_rmsnorm_backward_workspace(p.ranks, p.rows, p.cols) ||
+            (uintptr_t)p.workspace % 256)
+            return AR_ERR_INVALID_ARG;
+        if (bad_stride(p.rows, p.cols, &p.dy_stride) || bad_stride(p.rows, p.cols, &p.x_stride) ||
+            bad_stride(p.rows, p.cols, &p.dx_stride) ||
+            (p.dsum && bad_stride(p.rows, p.cols, &p.dsum_stride)))
+            return AR_ERR_INVALID_ARG;
+        if (misaligned(p.dy, p.dtype) || misaligned(p.x, p.dtype) || misaligned(p.dsum, p.dtype) ||
+            misaligned(p.dx, p.dtype) || misaligned(p.weight, p.weight_dtype) ||
+            misaligned(p.rstd, AR_FLOAT32))
+            return AR_ERR_INVALID_ARG;
+        const Rows outs[] = {
+            rows_of(p.dx, p.rows, p.cols, p.dx_stride, p.dtype),
+            rows_of(p.dweight, 1, (size_t)p.ranks * p.cols, 0, AR_FLOAT32),
+            {(uintptr_t)p.workspace, 1, ar_rmsnorm_backward_workspace(p.ranks, p.rows, p.cols), 0}};
+        const Rows ins[] = {rows_of(p.dy, p.rows, p.cols, p.dy_stride, p.dtype),
+                            rows_of(p.x, p.rows, p.cols, p.x_stride, p.dtype),
+                            rows_of(p.dsum, p.rows, p.cols, p.dsum_stride, p.dtype),
+                            rows_of(p.weight, 1, p.cols, 0, p.weight_dtype),
+                            rows_of(p.rstd, 1, p.rows, 0, AR_FLOAT32)};
+        if (!disjoint(outs, 3, ins, 5, 3))
+            return AR_ERR_INVALID_USAGE;
+    }
+    NormBackArgs a{};
+    a.dy = p.dy;
+    a.x = p.x;
+    a.weight = p.weight;
+    a.dsum = p.dsum;
+    a.rstd = p.rstd;
+    a.dx = p.dx;
+    a.dweight = p.dweight;
+    a.partial = static_cast<float*>(p.workspace);
+    a.rows_per_rank = p.rows / (size_t)p.ranks;
+    a.dy_stride = p.dy_stride;
+    a.x_stride = p.x_stride;
+    a.dsum_stride = p.dsum_stride;
+    a.dx_stride = p.dx_stride;
+    a.cols = (uint32_t)p.cols;
+    a.ranks = p.ranks;
+    a.blocks = norm_back_blocks(a.rows_per_rank, p.ranks);
+    a.weight_f32 = p.weight_dtype == AR_FLOAT32;
+    return done(launch_rmsnorm_back(p.dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+// ---- gradient lists ---------------------------------------------------------
+
+namespace {
+
+constexpr uint32_t kBf16Bit = 0x80000000u;
+// Largest tensor: its tiles, with those of a whole table, stay below 2^31.
+constexpr size_t kMaxSpan = (size_t)1 << 36;
+
+bool bad_span(const ar_span_t& s)
+{
+    return !stream_type(s.dtype) || s.count > kMaxSpan ||
+           (s.count && (!s.data || misaligned(s.data, s.dtype)));
+}
+
+uint32_t tiles_of(const ar_span_t& s)
+{
+    const uint64_t per = (uint64_t)kGradTileVecs * (16 / size_of(s.dtype));
+    return (uint32_t)((s.count + per - 1) / per);
+}
+
+// Workgroups for a table: a tile each while they are few.
+int grid_for(uint32_t tiles) { return (int)std::min<uint32_t>(tiles, kGradMaxBlocks); }
+
+// An output may be written while nothing else reads or writes its bytes.
+struct Reach {
+    uintptr_t lo, hi;
+    bool write;
+};
+
+bool clip_overlaps(const ar_span_t* in, const ar_span_t* out, size_t n, const float* norm)
+{
+    std::vector<Reach> v;
+    v.reserve(2 * n + 1);
+    for (size_t i = 0; i < n; ++i) {
+        const size_t bytes = in[i].count * size_of(in[i].dtype);
+        if (!bytes)
+            continue;
+        const uintptr_t a = (uintptr_t)in[i].data, b = (uintptr_t)out[i].data;
+        if (a != b)
+            v.push_back({a, a + bytes, false});
+        v.push_back({b, b + bytes, true});
+    }
+    v.push_back({(uintptr_t)norm, (uintptr_t)norm + 4, false});
+    const auto before = [](const Reach& x, const Reach& y) { return x.lo < y.lo; };
+    if (!std::is_sorted(v.begin(), v.end(), before))
+        std::sort(v.begin(), v.end(), before);
+    uintptr_t end_any = 0, end_write = 0;
+    for (const Reach& r : v) {
+        if (r.lo < (r.write ? end_any : end_write))
+            return true;
+        end_any = std::max(end_any, r.hi);
+        if (r.write)
+            end_write = std::max(end_write, r.hi);
+    }
+    return false;
+}
+
+}  // namespace
+
+namespace ar {
+
+int grad_norm_run(const ar_span_t* grads, size_t n, float* norm, double* partial, uint32_t* ticket,
+                  hipStream_t s, hipError_t* err)
+{
+    *err = hipSuccess;
+    if (!norm || misaligned(norm, AR_FLOAT32) || (n && !grads))
+        return AR_ERR_INVALID_ARG;
+    for (size_t i = 0; i < n; ++i) {
+        if (bad_span(grads[i]))
+            return AR_ERR_INVALID_ARG;
+        const uintptr_t at = (uintptr_t)grads[i].data, to = (uintptr_t)norm;
+        if (to < at + grads[i].count * size_of(grads[i].dtype) && at < to + sizeof(float) &&
+            grads[i].count)
+            return AR_ERR_INVALID_USAGE;
+    }
+    int live = 0;
+    size_t i = 0;
+    bool last = false;
+    while (!last) {
+        SpanTable t{};
+        for (; i < n && t.n < kSpansPerLaunch; ++i) {
+            const uint32_t tiles = tiles_of(grads[i]);
+            if (!tiles)
+                continue;
+            if (t.tiles + (uint64_t)tiles >= kBf16Bit)
+                break;
+            t.src[t.n] = grads[i].data;
+            t.count[t.n] = grads[i].count;
+            t.first[t.n] = t.tiles | (grads[i].dtype == AR_BF16 ? kBf16Bit : 0u);
+            t.tiles += tiles;
+            ++t.n;
+        }
+        while (i < n && !grads[i].count)
+            ++i;
+        last = i == n;
+        const int grid = std::max(1, grid_for(t.tiles));
+        *err = launch_grad_norm(t, partial, live, grid, ticket, last ? norm : nullptr, s);
+        if (*err != hipSuccess)
+            return AR_ERR_HIP;
+        live = std::max(live, grid);
+    }
+    return AR_SUCCESS;
+}
+
+}  // namespace ar
+
+extern "C" int ar_grad_clip(const ar_span_t* grads, const ar_span_t* out, size_t n,
+                            const float* norm, float max_norm, void* stream)
+{
+    if (!(max_norm >= 0.0f) || !norm || misaligned(norm, AR_FLOAT32) || (n && (!grads || !out)))
+        return AR_ERR_INVALID_ARG;
+    for (size_t i = 0; i < n; ++i)
+        if (bad_span(grads[i]) || bad_span(out[i]) || grads[i].count != out[i].count ||
+            grads[i].dtype != out[i].dtype)
+            return AR_ERR_INVALID_ARG;
+    try {
+        if (clip_overlaps(grads, out, n, norm))
+            return AR_ERR_INVALID_USAGE;
+    } catch (...) {
+        return AR_ERR_INTERNAL;
+    }
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    for (size_t i = 0; i < n;) {
+        SpanPairTable t{};
+        for (; i < n && t.n < kSpansPerLaunch; ++i) {
+            const uint32_t tiles = tiles_of(grads[i]);
+            if (!tiles)
+                continue;
+            if (t.tiles + (uint64_t)tiles >= kBf16Bit)
+                break;
+            t.src[t.n] = grads[i].data;
+            t.dst[t.n] = out[i].data;
+            t.count[t.n] = grads[i].count;
+            t.first[t.n] = t.tiles | (grads[i].dtype == AR_BF16 ? kBf16Bit : 0u);
+            t.tiles += tiles;
+            ++t.n;
+        }
+        if (!t.n)
+            break;
+        const hipError_t e = launch_grad_clip(t, norm, max_norm, grid_for(t.tiles), st);
+        if (e != hipSuccess)
+            return done(e);
+    }
+    return AR_SUCCESS;
+}

@@ -46,7 +46,10 @@ typedef struct ar_comm* ar_comm_t;
 /* Element type of send/recv.  AR_BF16 elements are 16-bit bfloat16 bit
  * patterns; they are added in float32 and rounded once (nearest-even) by the
  * rank that owns the element. */
-typedef enum { AR_INT32 = 0, AR_FLOAT32 = 1, AR_BF16 = 2 } ar_dtype_t;
+/* AR_E4M3 is an output type of the norms only (ar_rmsnorm): 8-bit floats with
+ * 4 exponent and 3 mantissa bits, no infinities, largest value 448; no
+ * collective moves it as such. */
+typedef enum { AR_INT32 = 0, AR_FLOAT32 = 1, AR_BF16 = 2, AR_E4M3 = 3 } ar_dtype_t;
 
 /* AR_RING: 2(R-1) steps around the ring q -> q+1, R-1 reduce-and-pass steps
  * then R-1 copy-and-pass steps ("GPU MODE lecture 68 notes", section 05,
@@ -382,13 +385,147 @@ int ar_stream_destroy(void* stream);
 int ar_ll_pingpong(void* lines, uint32_t* result_dev, int iters, int xcd_apart,
                    int64_t timeout_us, void* stream);
 
+/* ---- Operators around the collectives -------------------------------------
+ * What a training or serving step runs next to its collectives: the norm of
+ * the residual stream after the partial sums of tensor parallel ranks were
+ * reduced, its backward pass, and the global norm and clipping of reduced
+ * gradients.  No page defines them: they are this library's own.  All are
+ * asynchronous on `stream`, allocate nothing, keep nothing of one call for the
+ * next, and can be captured into a HIP graph; argument errors are reported by
+ * the return code, and nothing is enqueued then.  Sizes and strides are in
+ * elements.  Pointers need the alignment of their element type only (16-byte
+ * aligned rows are a little faster). */
+
+/* RMS norm with the residual's addition.  For each row t of `rows`:
+ *   h = x[t] + residual[t]                   (residual NULL: h = x[t])
+ *   r = 1 / sqrt(mean(h * h) + eps)
+ *   v = h * r * weight
+ * sum[t] receives h, y[t] receives v, rstd[t] receives r (sum and rstd may be
+ * NULL).  h, r and v are float32, and h enters the norm as it is before sum's
+ * rounding: every output is rounded once, to nearest even.  Sums of squares
+ * are float32; where they pass its range they are taken again in 64 bits.
+ * y in e4m3 (out_dtype AR_E4M3): a group is `group` consecutive columns (32,
+ * 64, 128 or 256; 0: the whole row; the row's last group may be shorter), its
+ * scale max(max |v| / 448, 2^-126) goes to scale[t][ceil(cols / group)], and y
+ * holds v / scale in e4m3.  A group with an infinity has an infinite
+ * scale, its infinities become NaN and the rest 0; one with a NaN is all NaN.
+ * x, residual, sum and y rows are `*_stride` apart (>= cols; ignored when
+ * rows is 1), columns are contiguous; scale and rstd are contiguous.  An
+ * output may share x's or residual's array, with the same address, stride and
+ * type; any other overlap of an output is AR_ERR_INVALID_USAGE (rows
+ * interleaved in one array with one stride do not overlap).
+ * rows == 0 or cols == 0 is a successful no-op.  cols is at most 2^30. */
+typedef struct {
+    int dtype;        /* AR_FLOAT32 or AR_BF16: x, residual, sum */
+    int out_dtype;    /* y: dtype, or AR_E4M3 */
+    int weight_dtype; /* weight: dtype, or AR_FLOAT32 */
+    float eps;        /* finite, >= 0 */
+    size_t rows, cols;
+    size_t group;
+    const void* x;
+    size_t x_stride;
+    const void* residual;
+    size_t residual_stride;
+    const void* weight;
+    void* sum;
+    size_t sum_stride;
+    void* y;
+    size_t y_stride;
+    float* scale; /* AR_E4M3 only (else ignored) */
+    float* rstd;
+} ar_rmsnorm_t;
+int ar_rmsnorm(const ar_rmsnorm_t* args, void* stream);
+
+/* Reduce-scatter with that norm behind it, in one pass over send: send is
+ * [R][R * tokens * cols] of the comm's dtype (float32 or bfloat16), each
+ * rank's partial sums of all R * tokens rows; rank q owns tokens [q * tokens,
+ * (q + 1) * tokens).  With x the reduction of the owner's tokens (the comm's
+ * AR_OPT_REDOP, sum or average, folded as ar_reduce_scatter's first channel
+ * folds, in float32 and not rounded), the rest is ar_rmsnorm with rows = R *
+ * tokens: residual, sum and y are [R][tokens * cols], rstd [R][tokens], scale
+ * [R][tokens * groups].  Of args, `rows` is the tokens of ONE rank; x, the
+ * strides and dtype are ignored (all arrays are contiguous, dtype is the
+ * comm's).  Needs no workspace.  AR_ERR_UNSUPPORTED for an int32 comm, for
+ * max / min, and for a comm set to AR_TREE; AR_ERR_INVALID_ARG when R *
+ * tokens * cols is above the comm's capacity. */
+int ar_reduce_scatter_rmsnorm(ar_comm_t comm, const void* send, const ar_rmsnorm_t* args,
+                              void* stream);
+
+/* Backward pass of the norm.  With n = x * r (x: the forward's h as it was
+ * stored, r: its rstd) and g = dy * weight, for each row:
+ *   dx = r * (g - n * mean(g * n)) + dsum      (dsum NULL: 0)
+ *   dweight = sum over rows of dy * n
+ * dx is the gradient of h, hence of both x and the residual; dsum is the
+ * gradient that reaches the stored sum from elsewhere.  The `rows` rows are
+ * `ranks` equal shards, one after the other (rows a multiple of ranks), and
+ * dweight is [ranks][cols] float32, a row for each rank's own tokens (an
+ * all-reduce of it gives every rank the whole gradient); ranks = 1 is the
+ * ordinary case.  All sums are float32, in an order that depends on sizes
+ * alone.  dx may be dy's, x's or dsum's array (same address, stride, type);
+ * else outputs must not overlap anything.  `workspace` is
+ * ar_rmsnorm_backward_workspace bytes of device memory, 256-byte aligned,
+ * whose contents mean nothing between calls.  rows == 0 writes zeros to
+ * dweight; cols == 0 is a no-op. */
+typedef struct {
+    int dtype;        /* AR_FLOAT32 or AR_BF16: dy, x, dsum, dx */
+    int weight_dtype; /* dtype, or AR_FLOAT32 */
+    int ranks;        /* 1 .. 64 */
+    size_t rows, cols;
+    const void* dy;
+    size_t dy_stride;
+    const void* x;
+    size_t x_stride;
+    const void* weight;
+    const float* rstd;
+    const void* dsum;
+    size_t dsum_stride;
+    void* dx;
+    size_t dx_stride;
+    float* dweight;
+    void* workspace;
+    size_t workspace_bytes;
+} ar_rmsnorm_backward_t;
+int ar_rmsnorm_backward(const ar_rmsnorm_backward_t* args, void* stream);
+size_t ar_rmsnorm_backward_workspace(int ranks, size_t rows, size_t cols);
+
+/* A tensor of a gradient list: `count` contiguous elements of AR_FLOAT32 or
+ * AR_BF16 (aligned to their size) at the device address `data`.  The arrays of
+ * spans are host memory, read during the call only. */
+typedef struct {
+    void* data;
+    size_t count;
+    int dtype;
+} ar_span_t;
+
+/* Global 2-norm of n tensors: norm[0] = sqrt(sum of the squares of all their
+ * elements), one float32 on the device, in any mixture of types.  Squares are
+ * added in 64-bit floats, in an order that depends on sizes and the device
+ * alone: no overflow or underflow in the sum, whatever the elements.  An
+ * infinity or NaN among them gives that.  n == 0, or only empty tensors: 0.
+ * Uses the comm's workspace (a ticket in its control block and 16 KiB of
+ * partial sums), so it is ordered with the comm's collectives as they are
+ * with each other. */
+int ar_grad_norm(ar_comm_t comm, const ar_span_t* grads, size_t n, float* norm, void* stream);
+
+/* Clipping by a norm on the device: out[i] = grads[i] * c for each of n
+ * tensors, c = max_norm / (norm[0] + 1e-6) where that is below 1, else 1 (NaN
+ * where the norm is), the product in float32 and rounded once.  out == grads,
+ * or out[i].data == grads[i].data, is in place (then nothing is written where
+ * c is 1); other overlaps, also of different tensors of the lists, are
+ * AR_ERR_INVALID_USAGE.  out[i] has grads[i]'s count and dtype.  The list may
+ * differ from the one whose norm was taken (all ranks' rows of a bucket, the
+ * norm over one of them).  max_norm: >= 0, no NaN. */
+int ar_grad_clip(const ar_span_t* grads, const ar_span_t* out, size_t n, const float* norm,
+                 float max_norm, void* stream);
+
 /* Message for a status code (static storage).  No page defines this call:
  * it is this library's own boundary design. */
 const char* ar_status_string(int status);
 
 /* Last hipError_t seen by this comm (0 if none); with comm == NULL, the last
  * one seen by the calling thread's utility calls (ar_stream_*,
- * ar_ll_pingpong). */
+ * ar_ll_pingpong) and calls without a comm (ar_rmsnorm, ar_rmsnorm_backward,
+ * ar_grad_clip). */
 int ar_last_hip_error(ar_comm_t comm);
 
 #ifdef __cplusplus
