@@ -164,7 +164,7 @@ struct ar_comm {
     uint64_t flag_stride = 0; // pipelined ring: ready flags per segment
     size_t off_rll = 0;       // ring-LL line slots
     uint64_t rll_cap = 0;     // ring-LL: lines per (sender, segment) per launch
-    size_t off_norm = 0;      // gradient norm: partial sums of kGradMaxBlocks workgroups
+    size_t off_norm = 0;      // gradient norm: partial sums and tickets (kGradScratchBytes)
     char* ws = nullptr;
     size_t ws_bytes = 0;
     // device facts, read on first use
@@ -889,7 +889,7 @@ int ar_init(ar_comm_t* out, int R, size_t count, ar_dtype_t dtype, ar_algo_t alg
     c->channels = std::min<int64_t>(std::max<int64_t>(1, env_int("AR_CHANNELS", 1)), c->nstrides);
     // workspace: control block | hand-off accumulators [cap] (A) | tree LL up
     // | down | tree epochs | pipelined flags | ring-LL lines | gradient norm's
-    // partial sums
+    // partial sums and tickets (cleared with the lines by ar_set_workspace)
     const size_t cap1 = count ? count : 1;
     c->tree_lines = std::min<uint64_t>((cap1 + 1) / 2, kTreeLinesCap);
     size_t off = kAlign;  // control block
@@ -919,7 +919,7 @@ int ar_init(ar_comm_t* out, int R, size_t count, ar_dtype_t dtype, ar_algo_t alg
                                     std::max<uint64_t>(64, (uint64_t)(1u << 21) / ((uint64_t)R * R)));
     off = align_up(off + (size_t)R * R * c->rll_cap * 8, kAlign);
     c->off_norm = off;
-    off = align_up(off + (size_t)kGradMaxBlocks * sizeof(double), kAlign);
+    off = align_up(off + kGradScratchBytes, kAlign);
     c->ws_need = off;
     *out = c;
     return AR_SUCCESS;
@@ -1154,8 +1154,7 @@ int ar_grad_norm(ar_comm_t c, const ar_span_t* grads, size_t n, float* norm, voi
         return AR_ERR_INVALID_USAGE;
     hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t e = hipSuccess;
-    const int rc = grad_norm_run(grads, n, norm, reinterpret_cast<double*>(c->ws + c->off_norm),
-                                 reinterpret_cast<uint32_t*>(c->ws) + kCtrlNormTicket, st, &e);
+    const int rc = grad_norm_run(grads, n, norm, c->ws + c->off_norm, st, &e);
     if (rc == AR_ERR_HIP)
         return fail_hip(c, e);
     if (rc == AR_SUCCESS)

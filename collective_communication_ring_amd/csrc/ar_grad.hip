@@ -1,8 +1,8 @@
 // ar_grad.hip -- the global 2-norm of many tensors, and their scaling by it.
 //
 // A launch takes a table of spans in its kernel arguments.  The tiles of all
-// its spans are numbered through; a workgroup takes a contiguous range of
-// them, so it looks its first span up once and then walks on.
+// its spans are numbered through; workgroup b takes tiles b, b + grid, ...,
+// with the next tile's loads in flight while it works on one.
 //
 // Squares are added in float64: every square of a float32 or bfloat16 is exact
 // there (48 bits or fewer) and inside its range, so the sum needs no scaling.
@@ -11,136 +11,197 @@
 namespace ar {
 namespace {
 
-constexpr uint32_t kIsBf16 = 0x80000000u;
+constexpr int kTileNV = kGradTileVecs / kBlock;  // a thread's vectors of a tile
 
-// The span that holds tile `t`: the last whose first tile is <= t.
+struct Tile {
+    uint32_t span;
+    uint64_t word;     // the span's
+    uint64_t offset;   // bytes from the span's start
+    uint32_t halves;   // 16-bit units
+    u32x4 r[kTileNV];
+};
+
+// The span that holds tile t is the last whose first tile is <= t.  Each lane
+// of the wave compares its own entries, in one round of loads; a search by
+// halves would wait for one entry after the other.
 template <class Table>
-__device__ inline int span_of(const Table& tab, uint32_t t)
+__device__ inline void find_tile(const Table& tab, uint32_t t, Tile* o)
 {
-    int lo = 0, hi = tab.n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((tab.first[mid] & ~kIsBf16) <= t)
-            lo = mid;
-        else
-            hi = mid;
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < Table::kSpans; k += 64)
+        n += __popcll(__ballot(tab.first[k + (threadIdx.x & 63u)] <= t));
+    const uint32_t s = (uint32_t)__builtin_amdgcn_readfirstlane(n) - 1;
+    o->span = s;
+    o->word = tab.span[s];
+    const uint32_t end = s + 1 < (uint32_t)tab.n ? tab.first[s + 1] : tab.tiles;
+    o->offset = (uint64_t)(t - tab.first[s]) * (kGradTileVecs * 16u);
+    o->halves = t + 1 == end ? ((uint32_t)(o->word >> 48) & 0x1fffu) + 1 : kGradTileHalves;
+}
+
+// All loads of a tile in flight together, the same for both types: whole
+// vectors, and the last vector of a cut-short tile by 16-bit units.  Non-
+// temporal: a list larger than the caches is read from memory twice anyway
+// (and one that fits the memory-side cache is served by it all the same).
+__device__ inline void load_tile(Tile* o)
+{
+    using Half = Elem<AR_BF16>;
+    const uint16_t* p = reinterpret_cast<const uint16_t*>((o->word & kSpanAddress) + o->offset);
+    if (o->halves == kGradTileHalves) {
+#pragma unroll
+        for (int k = 0; k < kTileNV; ++k)
+            o->r[k] = __builtin_nontemporal_load(
+                reinterpret_cast<const AnyVec<uint16_t>::type*>(p) + (k * kBlock + threadIdx.x));
+    } else {
+#pragma unroll
+        for (int k = 0; k < kTileNV; ++k)
+            o->r[k] = load_part<Half>(p, (k * kBlock + threadIdx.x) * 8u, o->halves);
     }
-    return lo;
+}
+
+// Calls work(tile) for each of this workgroup's tiles.
+template <class Table, class Work>
+__device__ inline void for_tiles(const Table& tab, Work work)
+{
+    uint32_t t = blockIdx.x;
+    if (t >= tab.tiles)
+        return;
+    Tile cur;
+    find_tile(tab, t, &cur);
+    load_tile(&cur);
+    for (;;) {
+        t += gridDim.x;
+        if (t >= tab.tiles || t < gridDim.x)
+            break;
+        Tile next;
+        find_tile(tab, t, &next);
+        load_tile(&next);
+        work(cur);
+        cur = next;
+    }
+    work(cur);
 }
 
 template <class E>
-__device__ inline double sum_tile(const void* src, uint64_t n, uint32_t tile)
+__device__ inline void add_squares(const Tile& tile, double (&acc)[2])
 {
-    using T = typename E::T;
-    constexpr uint64_t V = E::VEC;
-    const T* p = static_cast<const T*>(src);
-    const uint64_t lo = (uint64_t)tile * kGradTileVecs * V;
-    const uint64_t hi = lo + kGradTileVecs * V < n ? lo + kGradTileVecs * V : n;
-    double acc = 0.0;
-    for (uint64_t i = lo + threadIdx.x; i < hi; i += kBlock) {
-        const double v = (double)E::widen(p[i]);
-        acc = fma(v, v, acc);
+#pragma unroll
+    for (int k = 0; k < kTileNV; ++k) {
+        float v[E::VEC];
+        widen_slot<E, E::VEC>(tile.r[k], v);
+#pragma unroll
+        for (int i = 0; i < E::VEC; ++i)
+            acc[i & 1] = fma((double)v[i], (double)v[i], acc[i & 1]);
     }
-    return acc;
 }
 
-__global__ __launch_bounds__(kBlock) void k_grad_norm(SpanTable tab, double* partial, int live,
-                                                      uint32_t* ticket, float* norm)
+__device__ inline bool last_ticket(uint32_t* ticket, uint32_t of)
+{
+    return __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == of - 1;
+}
+
+__global__ __launch_bounds__(kBlock, 4) void k_grad_norm(SpanTable<kNormSpans> tab, double* slots,
+                                                         uint32_t* tickets, int live, float* norm)
 {
     constexpr int W = kBlock / 64;
     __shared__ double s_d[W];
     __shared__ uint32_t s_last;
-    const uint32_t lo = (uint32_t)((uint64_t)tab.tiles * blockIdx.x / gridDim.x);
-    const uint32_t hi = (uint32_t)((uint64_t)tab.tiles * (blockIdx.x + 1) / gridDim.x);
-    double acc = 0.0;
-    if (lo < hi) {
-        int s = span_of(tab, lo);
-        for (uint32_t t = lo; t < hi; ++t) {
-            while (s + 1 < tab.n && (tab.first[s + 1] & ~kIsBf16) <= t)
-                ++s;
-            const uint32_t first = tab.first[s];
-            const uint32_t tile = t - (first & ~kIsBf16);
-            acc += first & kIsBf16 ? sum_tile<Elem<AR_BF16>>(tab.src[s], tab.count[s], tile)
-                                   : sum_tile<Elem<AR_FLOAT32>>(tab.src[s], tab.count[s], tile);
-        }
-    }
+    double part[2] = {0.0, 0.0};
+    for_tiles(tab, [&](const Tile& tile) {
+        if (tile.word & kSpanBf16)
+            add_squares<Elem<AR_BF16>>(tile, part);
+        else
+            add_squares<Elem<AR_FLOAT32>>(tile, part);
+    });
+    double acc = part[0] + part[1];
     acc = block_sum<W>(acc, s_d);
-    // the slot is published before the ticket is taken (release), and whoever
-    // takes the last ticket sees every slot (acquire)
+    // A slot is stored through to memory, and is there before its workgroup's
+    // ticket is taken (the wait); whoever takes the last ticket reads all slots
+    // from there.  Release and acquire atomics would write back and drop the
+    // XCD's whole L2 for each workgroup.
     if (threadIdx.x == 0) {
         if ((int)blockIdx.x < live)
-            acc += partial[blockIdx.x];
-        __hip_atomic_store(partial + blockIdx.x, acc, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            acc += slots[blockIdx.x];
+        __hip_atomic_store(slots + blockIdx.x, acc, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         s_last = 0;
-        if (norm)
-            s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-                     gridDim.x - 1;
+        if (norm) {
+            __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
+            const uint32_t group = blockIdx.x / kTicketGroup;
+            const uint32_t groups = (gridDim.x + kTicketGroup - 1) / kTicketGroup;
+            const uint32_t left = gridDim.x - group * kTicketGroup;
+            uint32_t* mine = tickets + (group + 1) * kTicketLine;
+            if (last_ticket(mine, left < kTicketGroup ? left : kTicketGroup)) {
+                __hip_atomic_store(mine, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                s_last = last_ticket(tickets, groups);
+            }
+        }
     }
     __syncthreads();
     if (!s_last)
         return;
-    const int slots = live > (int)gridDim.x ? live : (int)gridDim.x;
+    const int n = live > (int)gridDim.x ? live : (int)gridDim.x;
     double sum = 0.0;
-    for (int i = threadIdx.x; i < slots; i += kBlock)
-        sum += __hip_atomic_load(partial + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int i = threadIdx.x; i < n; i += kBlock)
+        sum += __hip_atomic_load(slots + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     sum = block_sum<W>(sum, s_d);
     if (threadIdx.x == 0) {
         *norm = (float)sqrt(sum);
-        __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(tickets, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 
 template <class E>
-__device__ inline void clip_tile(const void* src, void* dst, uint64_t n, uint32_t tile, float coef)
+__device__ inline void store_scaled(const Tile& tile, void* dst, float coef)
 {
-    using T = typename E::T;
-    constexpr uint64_t V = E::VEC;
-    const T* p = static_cast<const T*>(src);
-    T* q = static_cast<T*>(dst);
-    const uint64_t lo = (uint64_t)tile * kGradTileVecs * V;
-    const uint64_t hi = lo + kGradTileVecs * V < n ? lo + kGradTileVecs * V : n;
-    for (uint64_t i = lo + threadIdx.x; i < hi; i += kBlock)
-        q[i] = E::narrow(E::widen(p[i]) * coef);
+    uint16_t* p = reinterpret_cast<uint16_t*>(static_cast<char*>(dst) + tile.offset);
+#pragma unroll
+    for (int k = 0; k < kTileNV; ++k) {
+        float v[E::VEC];
+        widen_slot<E, E::VEC>(tile.r[k], v);
+#pragma unroll
+        for (int i = 0; i < E::VEC; ++i)
+            v[i] *= coef;
+        const uint32_t at = k * kBlock + threadIdx.x;
+        if (tile.halves == kGradTileHalves)
+            __builtin_nontemporal_store(narrow_slot<E>(v),
+                                        reinterpret_cast<AnyVec<uint16_t>::type*>(p) + at);
+        else
+            store_part<Elem<AR_BF16>>(p, narrow_slot<E>(v), at * 8u, tile.halves);
+    }
 }
 
-__global__ __launch_bounds__(kBlock) void k_grad_clip(SpanPairTable tab, const float* norm,
-                                                      float max_norm)
+__global__ __launch_bounds__(kBlock, 4) void k_grad_clip(SpanTable<kClipSpans> tab, SpanOutputs out,
+                                                         const float* norm, float max_norm)
 {
-    const uint32_t lo = (uint32_t)((uint64_t)tab.tiles * blockIdx.x / gridDim.x);
-    const uint32_t hi = (uint32_t)((uint64_t)tab.tiles * (blockIdx.x + 1) / gridDim.x);
-    if (lo >= hi)
-        return;
     const float nv = *norm;
     const float c = max_norm / (nv + 1e-6f);
     const float coef = nv != nv ? nv : c < 1.0f ? c : 1.0f;
-    int s = span_of(tab, lo);
-    for (uint32_t t = lo; t < hi; ++t) {
-        while (s + 1 < tab.n && (tab.first[s + 1] & ~kIsBf16) <= t)
-            ++s;
-        if (coef == 1.0f && tab.src[s] == tab.dst[s])
-            continue;  // in place, unchanged
-        const uint32_t first = tab.first[s];
-        const uint32_t tile = t - (first & ~kIsBf16);
-        if (first & kIsBf16)
-            clip_tile<Elem<AR_BF16>>(tab.src[s], tab.dst[s], tab.count[s], tile, coef);
+    for_tiles(tab, [&](const Tile& tile) {
+        void* dst = out.dst[tile.span];
+        if (coef == 1.0f && (uintptr_t)dst == (tile.word & kSpanAddress))
+            return;  // in place, unchanged
+        if (tile.word & kSpanBf16)
+            store_scaled<Elem<AR_BF16>>(tile, dst, coef);
         else
-            clip_tile<Elem<AR_FLOAT32>>(tab.src[s], tab.dst[s], tab.count[s], tile, coef);
-    }
+            store_scaled<Elem<AR_FLOAT32>>(tile, dst, coef);
+    });
 }
 
 }  // namespace
 
-hipError_t launch_grad_norm(const SpanTable& t, double* partial, int live, int grid,
-                            uint32_t* ticket, float* norm, hipStream_t s)
+hipError_t launch_grad_norm(const SpanTable<kNormSpans>& t, void* scratch, int live, int grid, float* norm,
+                            hipStream_t s)
 {
-    hipLaunchKernelGGL(k_grad_norm, dim3(grid), dim3(kBlock), 0, s, t, partial, live, ticket, norm);
+    double* slots = static_cast<double*>(scratch);
+    hipLaunchKernelGGL(k_grad_norm, dim3(grid), dim3(kBlock), 0, s, t, slots,
+                       reinterpret_cast<uint32_t*>(slots + kGradMaxBlocks), live, norm);
     return hipGetLastError();
 }
 
-hipError_t launch_grad_clip(const SpanPairTable& t, const float* norm, float max_norm, int grid,
-                            hipStream_t s)
+hipError_t launch_grad_clip(const SpanTable<kClipSpans>& t, const SpanOutputs& o, const float* norm,
+                            float max_norm, int grid, hipStream_t s)
 {
-    hipLaunchKernelGGL(k_grad_clip, dim3(grid), dim3(kBlock), 0, s, t, norm, max_norm);
+    hipLaunchKernelGGL(k_grad_clip, dim3(grid), dim3(kBlock), 0, s, t, o, norm, max_norm);
     return hipGetLastError();
 }
 

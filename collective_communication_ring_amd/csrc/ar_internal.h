@@ -22,7 +22,6 @@ enum CtrlWord {
     kCtrlRingLLDone = 5,  // ring-LL: workgroups of the running launch that finished
     kCtrlPipeBase = 8,   // uint64 at words 8-9: the value every chunk flag holds between
                          // pipelined calls; a call of n steps raises it by n
-    kCtrlNormTicket = 10, // gradient norm: workgroups of the running launch that left their sum
     kCtrlWords = 64      // 256 bytes
 };
 

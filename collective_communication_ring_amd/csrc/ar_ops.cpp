@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <iterator>
 #include <vector>
 
 #include "ar_internal.h"
@@ -241,24 +242,46 @@ extern "C" int ar_rmsnorm_backward(const ar_rmsnorm_backward_t* args, void* stre
 
 namespace {
 
-constexpr uint32_t kBf16Bit = 0x80000000u;
-// Largest tensor: its tiles, with those of a whole table, stay below 2^31.
+// Largest tensor: the tiles of a whole table of such stay below 2^32 - 1.
 constexpr size_t kMaxSpan = (size_t)1 << 36;
 
 bool bad_span(const ar_span_t& s)
 {
-    return !stream_type(s.dtype) || s.count > kMaxSpan ||
+    return !stream_type(s.dtype) || s.count > kMaxSpan || ((uintptr_t)s.data & ~kSpanAddress) ||
            (s.count && (!s.data || misaligned(s.data, s.dtype)));
 }
 
-uint32_t tiles_of(const ar_span_t& s)
+// The next table of a list from span *i on, empty spans left out.
+template <class Table>
+void next_table(const ar_span_t* in, const ar_span_t* out, size_t n, size_t* i, Table* t,
+                SpanOutputs* o)
 {
-    const uint64_t per = (uint64_t)kGradTileVecs * (16 / size_of(s.dtype));
-    return (uint32_t)((s.count + per - 1) / per);
+    t->tiles = 0;
+    t->n = 0;
+    for (; *i < n && t->n < Table::kSpans; ++*i) {
+        const ar_span_t& s = in[*i];
+        if (!s.count)
+            continue;
+        const uint64_t halves = s.count * size_of(s.dtype) / 2;
+        const uint64_t tiles = (halves + kGradTileHalves - 1) / kGradTileHalves;
+        t->span[t->n] = pack_span(s.data, (uint32_t)(halves - (tiles - 1) * kGradTileHalves),
+                                  s.dtype == AR_BF16);
+        t->first[t->n] = t->tiles;
+        if (o)
+            o->dst[t->n] = out[*i].data;
+        t->tiles += (uint32_t)tiles;
+        ++t->n;
+    }
+    while (*i < n && !in[*i].count)
+        ++*i;
+    std::fill(t->first + t->n, std::end(t->first), 0xffffffffu);
 }
 
 // Workgroups for a table: a tile each while they are few.
-int grid_for(uint32_t tiles) { return (int)std::min<uint32_t>(tiles, kGradMaxBlocks); }
+int grid_for(uint32_t tiles)
+{
+    return (int)std::max<uint32_t>(1, std::min<uint32_t>(tiles, kGradMaxBlocks));
+}
 
 // An output may be written while nothing else reads or writes its bytes.
 struct Reach {
@@ -298,8 +321,8 @@ bool clip_overlaps(const ar_span_t* in, const ar_span_t* out, size_t n, const fl
 
 namespace ar {
 
-int grad_norm_run(const ar_span_t* grads, size_t n, float* norm, double* partial, uint32_t* ticket,
-                  hipStream_t s, hipError_t* err)
+int grad_norm_run(const ar_span_t* grads, size_t n, float* norm, void* scratch, hipStream_t s,
+                  hipError_t* err)
 {
     *err = hipSuccess;
     if (!norm || misaligned(norm, AR_FLOAT32) || (n && !grads))
@@ -314,30 +337,15 @@ int grad_norm_run(const ar_span_t* grads, size_t n, float* norm, double* partial
     }
     int live = 0;
     size_t i = 0;
-    bool last = false;
-    while (!last) {
-        SpanTable t{};
-        for (; i < n && t.n < kSpansPerLaunch; ++i) {
-            const uint32_t tiles = tiles_of(grads[i]);
-            if (!tiles)
-                continue;
-            if (t.tiles + (uint64_t)tiles >= kBf16Bit)
-                break;
-            t.src[t.n] = grads[i].data;
-            t.count[t.n] = grads[i].count;
-            t.first[t.n] = t.tiles | (grads[i].dtype == AR_BF16 ? kBf16Bit : 0u);
-            t.tiles += tiles;
-            ++t.n;
-        }
-        while (i < n && !grads[i].count)
-            ++i;
-        last = i == n;
-        const int grid = std::max(1, grid_for(t.tiles));
-        *err = launch_grad_norm(t, partial, live, grid, ticket, last ? norm : nullptr, s);
+    do {  // a list of nothing has one table, of no spans: its norm is 0
+        SpanTable<kNormSpans> t;
+        next_table(grads, nullptr, n, &i, &t, nullptr);
+        const int grid = grid_for(t.tiles);
+        *err = launch_grad_norm(t, scratch, live, grid, i == n ? norm : nullptr, s);
         if (*err != hipSuccess)
             return AR_ERR_HIP;
         live = std::max(live, grid);
-    }
+    } while (i < n);
     return AR_SUCCESS;
 }
 
@@ -358,25 +366,14 @@ extern "C" int ar_grad_clip(const ar_span_t* grads, const ar_span_t* out, size_t
     } catch (...) {
         return AR_ERR_INTERNAL;
     }
-    hipStream_t st = static_cast<hipStream_t>(stream);
     for (size_t i = 0; i < n;) {
-        SpanPairTable t{};
-        for (; i < n && t.n < kSpansPerLaunch; ++i) {
-            const uint32_t tiles = tiles_of(grads[i]);
-            if (!tiles)
-                continue;
-            if (t.tiles + (uint64_t)tiles >= kBf16Bit)
-                break;
-            t.src[t.n] = grads[i].data;
-            t.dst[t.n] = out[i].data;
-            t.count[t.n] = grads[i].count;
-            t.first[t.n] = t.tiles | (grads[i].dtype == AR_BF16 ? kBf16Bit : 0u);
-            t.tiles += tiles;
-            ++t.n;
-        }
+        SpanTable<kClipSpans> t;
+        SpanOutputs o;
+        next_table(grads, out, n, &i, &t, &o);
         if (!t.n)
             break;
-        const hipError_t e = launch_grad_clip(t, norm, max_norm, grid_for(t.tiles), st);
+        const hipError_t e = launch_grad_clip(t, o, norm, max_norm, grid_for(t.tiles),
+                                              static_cast<hipStream_t>(stream));
         if (e != hipSuccess)
             return done(e);
     }

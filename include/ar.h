@@ -502,9 +502,9 @@ typedef struct {
  * added in 64-bit floats, in an order that depends on sizes and the device
  * alone: no overflow or underflow in the sum, whatever the elements.  An
  * infinity or NaN among them gives that.  n == 0, or only empty tensors: 0.
- * Uses the comm's workspace (a ticket in its control block and 16 KiB of
- * partial sums), so it is ordered with the comm's collectives as they are
- * with each other. */
+ * Uses the comm's workspace (6.2 KiB of partial sums and counters at its
+ * end), so it is ordered with the comm's collectives as they are with each
+ * other. */
 int ar_grad_norm(ar_comm_t comm, const ar_span_t* grads, size_t n, float* norm, void* stream);
 
 /* Clipping by a norm on the device: out[i] = grads[i] * c for each of n
