@@ -39,8 +39,7 @@ __device__ inline void find_tile(const Table& tab, uint32_t t, Tile* o)
     o->halves = t + 1 == end ? ((uint32_t)(o->word >> 48) & 0x1fffu) + 1 : kGradTileHalves;
 }
 
-// All loads of a tile in flight together, the same for both types: whole
-// vectors, and the last vector of a cut-short tile by 16-bit units.  Non-
+// All loads of a tile in flight together, the same for both types.  Non-
 // temporal: a list larger than the caches is read from memory twice anyway
 // (and one that fits the memory-side cache is served by it all the same).
 __device__ inline void load_tile(Tile* o)
@@ -52,11 +51,30 @@ __device__ inline void load_tile(Tile* o)
         for (int k = 0; k < kTileNV; ++k)
             o->r[k] = __builtin_nontemporal_load(
                 reinterpret_cast<const AnyVec<uint16_t>::type*>(p) + (k * kBlock + threadIdx.x));
-    } else {
+    } else if (o->halves >= Half::VEC) {
 #pragma unroll
         for (int k = 0; k < kTileNV; ++k)
-            o->r[k] = load_part<Half>(p, (k * kBlock + threadIdx.x) * 8u, o->halves);
+            o->r[k] = load_vec<Half>(p, (k * kBlock + threadIdx.x) * 8u, o->halves);
+    } else {
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int k = 0; k < kTileNV; ++k)
+            o->r[k] = zero;
+        if (threadIdx.x == 0)
+            for (uint32_t i = 0; i < o->halves; ++i)
+                o->r[0][i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
     }
+}
+
+// Before a tile's vectors are used: a cut-short tile's last one is moved into
+// place, and those past its end are zero.
+__device__ inline void fit_tile(Tile* o)
+{
+    using Half = Elem<AR_BF16>;
+    if (o->halves != kGradTileHalves && o->halves >= Half::VEC)
+#pragma unroll
+        for (int k = 0; k < kTileNV; ++k)
+            fit<Half>(o->r[k], (k * kBlock + threadIdx.x) * 8u, o->halves);
 }
 
 // Calls work(tile) for each of this workgroup's tiles.
@@ -76,9 +94,11 @@ __device__ inline void for_tiles(const Table& tab, Work work)
         Tile next;
         find_tile(tab, t, &next);
         load_tile(&next);
+        fit_tile(&cur);
         work(cur);
         cur = next;
     }
+    fit_tile(&cur);
     work(cur);
 }
 
@@ -161,12 +181,8 @@ __device__ inline void store_scaled(const Tile& tile, void* dst, float coef)
 #pragma unroll
         for (int i = 0; i < E::VEC; ++i)
             v[i] *= coef;
-        const uint32_t at = k * kBlock + threadIdx.x;
-        if (tile.halves == kGradTileHalves)
-            __builtin_nontemporal_store(narrow_slot<E>(v),
-                                        reinterpret_cast<AnyVec<uint16_t>::type*>(p) + at);
-        else
-            store_part<Elem<AR_BF16>>(p, narrow_slot<E>(v), at * 8u, tile.halves);
+        store_vec<Elem<AR_BF16>, true>(p, narrow_slot<E>(v), (k * kBlock + threadIdx.x) * 8u,
+                                       tile.halves);
     }
 }
 

@@ -11,6 +11,13 @@
 namespace ar {
 namespace {
 
+// Vectors of a call up to which its rows are spread over as many waves as they
+// can use (one vector a thread): 16 waves on each CU.  Below, that is faster
+// (bf16 513 x 2048: 4.5 us, two vectors a thread 5.2; 8 ranks' 8 x 4096: 4.1
+// and 5.0), above, two vectors are (8192 x 8192: 75 us, one 95; 8193 x 2571: 33
+// us, one 37).  Four are for the longest rows alone (8193 x 2571: 38 us).
+constexpr uint64_t kFewVecs = 256 * 16 * 64;
+
 // Any row length, one workgroup per row, an element at a time: pass 1 sums the
 // squares, pass 2 writes; e4m3 takes the groups' largest values between them.
 // Each pass reads the row again (from L2, except the first).  A thread reads
@@ -101,39 +108,63 @@ __global__ __launch_bounds__(kBlock) void k_norm_any(NormArgs a)
     }
 }
 
-// Rows that fit in registers: TPR threads per row (64: a wave each, four rows
-// to a workgroup), NV vectors per thread, vector k of a row's thread l at
-// column (k TPR + l) VEC.  One pass: every input is read once, all loads of a
-// row in flight together, and h stays in registers through the sum of squares
-// and the groups' largest values.  A thread has read its own elements of all
-// inputs before it writes them, and no other thread touches them, so an output
-// may be an input's array.
-template <class E, bool WF32, bool Q, int TPR, int NV, bool MULTI>
-__global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void k_norm(NormArgs a)
+// A row's vectors from registers.  The exact and the other case, and the two
+// kinds of store, are told apart once for all of them: tested at each store
+// they cost bf16 8192 x 8192 81 us instead of 75.
+template <class E, int NV>
+__device__ inline void store_row(typename E::T* p, const float (&v)[NV][E::VEC], uint32_t lane,
+                                 const NormArgs& a)
+{
+    if (a.exact && a.stream) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            store_whole<E, true>(p + (k * a.lanes + lane) * E::VEC, narrow_slot<E>(v[k]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            store_vec<E, false>(p, narrow_slot<E>(v[k]), (k * a.lanes + lane) * E::VEC, a.cols);
+    }
+}
+
+// Rows of at least a vector that fit in registers: a.lanes threads per row (a
+// power of two below 64, or 64 for each of its waves), NV vectors per thread,
+// vector k of thread l at column (k lanes + l) VEC.  A workgroup is one row of
+// several waves, or as many shorter rows as 256 threads hold.  One pass: every
+// input is read once, all loads of a row in flight together, and h stays in
+// registers through the sum of squares and the groups' largest values.  A
+// thread has read its own elements of all inputs before it writes them, and no
+// other thread uses them, so an output may be an input's array.
+//
+// Bound by memory: bf16 8192 x 8192 with residual and e4m3 output moves its 472
+// MB in 75 us (6.3 TB/s; a copy of 1 GiB: 5.9).
+template <class E, bool WF32, bool Q, int NV, bool MULTI, int MAXT>
+__global__ __launch_bounds__(MAXT) void k_norm(NormArgs a)
 {
     using T = typename E::T;
     constexpr int V = E::VEC;
-    constexpr int W = TPR / 64;
-    constexpr int ROWS = TPR < kBlock ? kBlock / TPR : 1;
-    __shared__ float s_f[W];
-    __shared__ double s_d[W];
-    __shared__ uint32_t s_u[W];
-    const uint32_t lane = threadIdx.x % TPR;
-    const uint64_t t = (uint64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
-    if (t >= a.rows)  // a whole wave's rows (TPR == 64), never a part of a workgroup's row
+    __shared__ float s_f[kMaxWaves];
+    __shared__ double s_d[kMaxWaves];
+    __shared__ uint32_t s_u[kMaxWaves];
+    const uint32_t lanes = a.lanes, wave = threadIdx.x >> 6;
+    const uint32_t lane = lanes <= 64 ? threadIdx.x & (lanes - 1) : threadIdx.x;
+    const uint64_t t = lanes <= 64 ? ((uint64_t)blockIdx.x * blockDim.x + threadIdx.x) / lanes
+                                   : blockIdx.x;
+    if (t >= a.rows)  // all threads of a row; rows of several waves have no such workgroup
         return;
+    const auto column = [&](int k) { return (k * lanes + lane) * V; };
     const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
     float h[NV][V];
     u32x4 res[NV];
+    Weight<E, WF32> w[NV];
     if (a.residual) {
         const T* r = static_cast<const T*>(a.residual) + t * a.res_stride;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            res[k] = load_part<E>(r, (k * TPR + lane) * V, a.cols);
+            res[k] = load_vec<E>(r, column(k), a.cols);
     }
     if constexpr (MULTI) {
         // U ranks' vectors in flight at a time, added in the ring's order
-        constexpr int U = NV >= 4 ? (TPR > 512 ? 1 : 2) : NV >= 2 ? 4 : 8;
+        constexpr int U = NV >= 4 ? (MAXT > 256 ? 1 : 2) : NV >= 2 ? 4 : 8;
         int p = (int)(t / a.tokens_per_rank);
         for (int i0 = 0; i0 < a.parts; i0 += U) {
             u32x4 raw[U][NV];
@@ -144,7 +175,7 @@ __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void k_norm(NormArgs a
                     const T* q = x + (uint64_t)p * a.part_stride;
 #pragma unroll
                     for (int k = 0; k < NV; ++k)
-                        raw[u][k] = load_part<E>(q, (k * TPR + lane) * V, a.cols);
+                        raw[u][k] = load_vec<E>(q, column(k), a.cols);
                 }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -152,6 +183,8 @@ __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void k_norm(NormArgs a
 #pragma unroll
                     for (int k = 0; k < NV; ++k) {
                         float v[V];
+                        if (!a.exact)
+                            fit<E>(raw[u][k], column(k), a.cols);
                         widen_slot<E, V>(raw[u][k], v);
 #pragma unroll
                         for (int i = 0; i < V; ++i)
@@ -159,6 +192,9 @@ __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void k_norm(NormArgs a
                     }
                 }
         }
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            w[k].load(a.weight, column(k), a.cols);
         if (a.divisor != 1.0f)
 #pragma unroll
             for (int k = 0; k < NV; ++k)
@@ -169,15 +205,25 @@ __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void k_norm(NormArgs a
         u32x4 raw[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            raw[k] = load_part<E>(x, (k * TPR + lane) * V, a.cols);
+            raw[k] = load_vec<E>(x, column(k), a.cols);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            w[k].load(a.weight, column(k), a.cols);
+        if (!a.exact)
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                fit<E>(raw[k], column(k), a.cols);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             widen_slot<E, V>(raw[k], h[k]);
     }
-    float w[NV][V];
+    if (!a.exact)
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-        load_weight<E, WF32>(a.weight, (k * TPR + lane) * V, a.cols, w[k]);
+        for (int k = 0; k < NV; ++k) {
+            w[k].fit_to(column(k), a.cols);
+            if (a.residual)
+                fit<E>(res[k], column(k), a.cols);
+        }
     if (a.residual)
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -187,19 +233,15 @@ __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void k_norm(NormArgs a
             for (int i = 0; i < V; ++i)
                 h[k][i] += v[i];
         }
-    if (a.sum) {
-        T* sum = static_cast<T*>(a.sum) + t * a.sum_stride;
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-            store_part<E>(sum, narrow_slot<E>(h[k]), (k * TPR + lane) * V, a.cols);
-    }
+    if (a.sum)
+        store_row<E, NV>(static_cast<T*>(a.sum) + t * a.sum_stride, h, lane, a);
     float ss = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < V; ++i)
             ss = fmaf(h[k][i], h[k][i], ss);
-    ss = block_sum<W>(ss, s_f);
+    ss = row_total(ss, s_f, wave, lanes);
     const float r = inv_rms(ss, a.cols, a.eps, [&] {
         double d = 0.0;
 #pragma unroll
@@ -207,15 +249,18 @@ __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void k_norm(NormArgs a
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 d = fma((double)h[k][i], (double)h[k][i], d);
-        return block_sum<W>(d, s_d);
+        return row_total(d, s_d, wave, lanes);
     });
     if (a.rstd && lane == 0)
         a.rstd[t] = r;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+        float v[V];
+        w[k].get(v);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            h[k][i] = h[k][i] * r * w[k][i];
+            h[k][i] = h[k][i] * r * v[i];
+    }
     if constexpr (Q) {
         uint8_t* y = static_cast<uint8_t*>(a.y) + t * a.y_stride;
         uint32_t m[NV];
@@ -225,7 +270,7 @@ __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void k_norm(NormArgs a
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 // past the row's end: 0, or NaN where r is infinite or NaN
-                if ((k * TPR + lane) * V + i < a.cols)
+                if (column(k) + i < a.cols)
                     m[k] = umax(m[k], __float_as_uint(h[k][i]) & 0x7fffffffu);
         }
         if (a.groups == 1) {
@@ -233,7 +278,7 @@ __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void k_norm(NormArgs a
 #pragma unroll
             for (int k = 1; k < NV; ++k)
                 all = umax(all, m[k]);
-            all = block_umax<W>(all, s_u);
+            all = row_umax(all, s_u, wave, lanes);
 #pragma unroll
             for (int k = 0; k < NV; ++k)
                 m[k] = all;
@@ -244,71 +289,62 @@ __global__ __launch_bounds__(TPR < kBlock ? kBlock : TPR) void k_norm(NormArgs a
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const uint32_t c = (k * TPR + lane) * V;
+            const uint32_t c = column(k);
             const float scale = e4m3_scale(m[k]);
             const float inv = 1.0f / scale;
             if (c < a.cols && c % a.group == 0)
                 a.scale[t * a.groups + c / a.group] = scale;
-            uint32_t q[V / 4];
+            u32x4 q = {0u, 0u, 0u, 0u};
 #pragma unroll
             for (int j = 0; j < V / 4; ++j)
                 q[j] = e4m3x4(h[k][4 * j] * inv, h[k][4 * j + 1] * inv, h[k][4 * j + 2] * inv,
                               h[k][4 * j + 3] * inv);
             if (c + V <= a.cols) {
-                if constexpr (V == 8) {
-                    typedef uint32_t u32x2 __attribute__((ext_vector_type(2), aligned(1)));
+                // plain stores also where the others stream: 8 bytes a lane fill
+                // half a wave's lines (both streamed: 79 us of the 75)
+                typedef uint32_t u32x2 __attribute__((ext_vector_type(2), aligned(1)));
+                typedef uint32_t u32 __attribute__((aligned(1)));
+                if constexpr (V == 8)
                     *reinterpret_cast<u32x2*>(y + c) = u32x2{q[0], q[1]};
-                } else {
-                    typedef uint32_t u32x1 __attribute__((aligned(1)));
-                    *reinterpret_cast<u32x1*>(y + c) = q[0];
-                }
+                else
+                    *reinterpret_cast<u32*>(y + c) = q[0];
             } else if (c < a.cols) {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (c + i < a.cols)
-                        y[c + i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+                store_head(y + c, q, a.cols - c);
             }
         }
     } else {
-        T* y = static_cast<T*>(a.y) + t * a.y_stride;
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-            store_part<E>(y, narrow_slot<E>(h[k]), (k * TPR + lane) * V, a.cols);
+        store_row<E, NV>(static_cast<T*>(a.y) + t * a.y_stride, h, lane, a);
     }
 }
 
-template <class E, bool WF32, bool Q, int TPR, int NV, bool MULTI>
-void launch_row(const NormArgs& a, hipStream_t s)
+template <class E, bool WF32, bool Q, int NV, bool MULTI, int MAXT>
+void launch_row(NormArgs a, uint32_t nvec, hipStream_t s)
 {
-    constexpr int threads = TPR < kBlock ? kBlock : TPR;
-    constexpr int rows = threads / TPR;
-    hipLaunchKernelGGL((k_norm<E, WF32, Q, TPR, NV, MULTI>),
-                       dim3((unsigned)((a.rows + rows - 1) / rows)), dim3(threads), 0, s, a);
+    a.lanes = 64 * ((nvec + 64 * NV - 1) / (64 * NV));
+    if (NV == 1)
+        while (a.lanes <= 64 && a.lanes / 2 >= nvec && a.lanes > 1)
+            a.lanes /= 2;
+    a.exact = a.cols == NV * a.lanes * E::VEC;
+    const uint32_t rows = a.lanes <= 64 ? kBlock / a.lanes : 1;
+    hipLaunchKernelGGL((k_norm<E, WF32, Q, NV, MULTI, MAXT>),
+                       dim3((unsigned)((a.rows + rows - 1) / rows)), dim3(a.lanes * rows), 0, s, a);
 }
 
 template <class E, bool WF32, bool Q, bool MULTI>
 void launch_typed(const NormArgs& a, hipStream_t s)
 {
     const uint32_t nvec = (a.cols + E::VEC - 1) / E::VEC;
-    // rows past 2^31 workgroups and rows longer than 4096 vectors go an
-    // element at a time
-    if (a.rows > 1u << 30 || nvec > 4096)
+    // rows of less than a vector, of more than 4096, and more rows than a grid
+    // holds go an element at a time
+    if (a.cols < E::VEC || nvec > 64 * 4 * kMaxWaves || a.rows > 1u << 30)
         hipLaunchKernelGGL((k_norm_any<E, Q>), dim3((unsigned)std::min<uint64_t>(a.rows, 1u << 16)),
                            dim3(kBlock), 0, s, a);
-    else if (nvec <= 64)
-        launch_row<E, WF32, Q, 64, 1, MULTI>(a, s);
-    else if (nvec <= 128)
-        launch_row<E, WF32, Q, 64, 2, MULTI>(a, s);
-    else if (nvec <= 256)
-        launch_row<E, WF32, Q, 256, 1, MULTI>(a, s);
-    else if (nvec <= 512)
-        launch_row<E, WF32, Q, 256, 2, MULTI>(a, s);
-    else if (nvec <= 1024)
-        launch_row<E, WF32, Q, 256, 4, MULTI>(a, s);
-    else if (nvec <= 2048)
-        launch_row<E, WF32, Q, 512, 4, MULTI>(a, s);
+    else if (nvec > 64 * 2 * kMaxWaves)
+        launch_row<E, WF32, Q, 4, MULTI, 1024>(a, nvec, s);
+    else if (nvec <= 64 || (nvec <= 64 * kMaxWaves && a.rows * nvec <= kFewVecs))
+        launch_row<E, WF32, Q, 1, MULTI, 1024>(a, nvec, s);
     else
-        launch_row<E, WF32, Q, 1024, 4, MULTI>(a, s);
+        launch_row<E, WF32, Q, 2, MULTI, 1024>(a, nvec, s);
 }
 
 template <class E, bool WF32, bool Q>
@@ -325,8 +361,9 @@ void launch_out(bool e4m3, const NormArgs& a, hipStream_t s)
 
 }  // namespace
 
-hipError_t launch_rmsnorm(int dtype, bool e4m3, const NormArgs& a, hipStream_t s)
+hipError_t launch_rmsnorm(int dtype, bool e4m3, NormArgs a, hipStream_t s)
 {
+    a.stream = a.rows * a.cols * (dtype == AR_BF16 ? 2 : 4) > kStreamBytes;
     if (dtype == AR_FLOAT32)
         launch_out<Elem<AR_FLOAT32>, false>(e4m3, a, s);
     else if (a.weight_f32)

@@ -1,6 +1,8 @@
 // ar_norm_common.h -- pieces the norm's forward and backward kernels share.
 #pragma once
 
+#include <type_traits>
+
 #include "ar_elem.h"
 #include "ar_internal.h"
 #include "ar_ops.h"
@@ -29,6 +31,29 @@ __device__ inline float row_sum(float v)
     return v;
 }
 
+// Sum over aligned runs of `lanes` (a power of two, 32 at most).
+__device__ inline float lanes_sum(float v, uint32_t lanes)
+{
+    if (lanes > 1)
+        v += __uint_as_float(dpp<kXor1>(__float_as_uint(v)));
+    if (lanes > 2)
+        v += __uint_as_float(dpp<kXor2>(__float_as_uint(v)));
+    if (lanes > 4)
+        v += __uint_as_float(dpp<kMirror8>(__float_as_uint(v)));
+    if (lanes > 8)
+        v += __uint_as_float(dpp<kMirror16>(__float_as_uint(v)));
+    if (lanes > 16)
+        v += __shfl_xor(v, 16);
+    return v;
+}
+
+__device__ inline double lanes_sum(double v, uint32_t lanes)
+{
+    for (uint32_t d = 1; d < lanes; d <<= 1)
+        v += __shfl_xor(v, (int)d);
+    return v;
+}
+
 __device__ inline float lane_of(float v, int lane)
 {
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
@@ -40,13 +65,7 @@ __device__ inline float wave_sum(float v)
     return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 
-__device__ inline double wave_sum(double v)
-{
-#pragma unroll
-    for (int d = 32; d; d >>= 1)
-        v += __shfl_xor(v, d);
-    return v;
-}
+__device__ inline double wave_sum(double v) { return lanes_sum(v, 64u); }
 
 __device__ inline uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
@@ -109,6 +128,50 @@ __device__ inline uint32_t block_umax(uint32_t v, uint32_t* s)
     return v;
 }
 
+// The same over a row's `lanes`: a power of two below 64, or 64 for each of its
+// waves (16 at most; the calling one's number is w).  Each array `s` is used
+// once between barriers: every lane reads one wave's value, and a fold over 16
+// lanes leaves the whole on all.
+__device__ inline float row_total(float v, float* s, uint32_t w, uint32_t lanes)
+{
+    if (lanes < 64)
+        return lanes_sum(v, lanes);
+    v = wave_sum(v);
+    if (lanes == 64)
+        return v;
+    if ((threadIdx.x & 63u) == 0)
+        s[w] = v;
+    __syncthreads();
+    const uint32_t l = threadIdx.x & 15u;
+    return row_sum(l * 64 < lanes ? s[l] : 0.0f);
+}
+
+__device__ inline double row_total(double v, double* s, uint32_t w, uint32_t lanes)
+{
+    if (lanes <= 64)
+        return lanes_sum(v, lanes);
+    v = wave_sum(v);
+    if ((threadIdx.x & 63u) == 0)
+        s[w] = v;
+    __syncthreads();
+    v = 0.0;
+    for (uint32_t k = 0; k * 64 < lanes; ++k)
+        v += s[k];
+    return v;
+}
+
+__device__ inline uint32_t row_umax(uint32_t v, uint32_t* s, uint32_t w, uint32_t lanes)
+{
+    v = lanes_umax(v, lanes < 64 ? lanes : 64u);
+    if (lanes <= 64)
+        return v;
+    if ((threadIdx.x & 63u) == 0)
+        s[w] = v;
+    __syncthreads();
+    const uint32_t l = threadIdx.x & 15u;
+    return lanes_umax(l * 64 < lanes ? s[l] : 0u, 16);
+}
+
 // r = 1 / sqrt(mean + eps).  A float32 sum of squares that is infinite may
 // have overflowed from finite elements: `again` then takes it in 64 bits.
 template <class Again>
@@ -158,36 +221,93 @@ struct AnyVec<uint16_t> {
     typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2)));
 };
 
-// Elements [c, c + VEC) of a row of `cols`; those past its end read as zero.
-// Only a row's last vector can be cut short, and it goes element by element.
+// The vector of elements [c, c + VEC) of a row of `cols` >= VEC elements.  One
+// that would reach past the row's end is read where it ends there, so that a
+// row's loads are all alike and in flight together; fit() then puts it right,
+// where it is used.  (A cut-short vector read element by element cost a row of
+// 2571 bfloat16 a third of its time: a chain of waits in its last wave.)
 template <class E>
-__device__ inline u32x4 load_part(const typename E::T* p, uint32_t c, uint32_t cols)
+__device__ inline u32x4 load_vec(const typename E::T* p, uint32_t c, uint32_t cols)
 {
-    using T = typename E::T;
-    u32x4 r = {0u, 0u, 0u, 0u};
-    if (c + E::VEC <= cols) {
-        r = __builtin_nontemporal_load(reinterpret_cast<const typename AnyVec<T>::type*>(p + c));
-    } else if (c < cols) {
-#pragma unroll
-        for (int i = 0; i < E::VEC; ++i)
-            if (c + i < cols)
-                r[i * sizeof(T) / 4] |= E::t_bits(p[c + i]) << (8 * (i * sizeof(T) % 4));
-    }
-    return r;
+    const uint32_t at = c + E::VEC <= cols ? c : cols - E::VEC;
+    return __builtin_nontemporal_load(
+        reinterpret_cast<const typename AnyVec<typename E::T>::type*>(p + at));
 }
 
+// Moves what load_vec read for column c there; elements past the end are zero.
 template <class E>
-__device__ inline void store_part(typename E::T* p, const u32x4& r, uint32_t c, uint32_t cols)
+__device__ inline void fit(u32x4& r, uint32_t c, uint32_t cols)
 {
-    using T = typename E::T;
-    if (c + E::VEC <= cols) {
-        *reinterpret_cast<typename AnyVec<T>::type*>(p + c) = r;
-    } else if (c < cols) {
+    if (c + E::VEC <= cols)
+        return;
+    uint32_t drop = (c < cols ? c + E::VEC - cols : E::VEC) * (uint32_t)sizeof(typename E::T) * 8;
+    uint64_t lo = (uint64_t)r[1] << 32 | r[0], hi = (uint64_t)r[3] << 32 | r[2];
 #pragma unroll
-        for (int i = 0; i < E::VEC; ++i)
-            if (c + i < cols)
-                p[c + i] = E::t_from_bits(r[i * sizeof(T) / 4] >> (8 * (i * sizeof(T) % 4)));
+    for (int i = 0; i < 2; ++i)
+        if (drop >= 64) {
+            lo = hi;
+            hi = 0;
+            drop -= 64;
+        }
+    if (drop) {
+        lo = lo >> drop | hi << (64 - drop);
+        hi >>= drop;
     }
+    r = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// The first n (< 16 / sizeof(U)) units of a vector, in at most log2 stores.
+template <class U>
+__device__ inline void store_head(U* p, const u32x4& r, uint32_t n)
+{
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2), aligned(1)));
+    typedef uint32_t u32 __attribute__((aligned(1)));
+    uint64_t left = (uint64_t)r[1] << 32 | r[0];
+    if (n * sizeof(U) & 8) {
+        *reinterpret_cast<u32x2*>(p) = u32x2{r[0], r[1]};
+        p += 8 / sizeof(U);
+        left = (uint64_t)r[3] << 32 | r[2];
+    }
+    uint32_t word = (uint32_t)left;
+    if (n * sizeof(U) & 4) {
+        *reinterpret_cast<u32*>(p) = word;
+        p += 4 / sizeof(U);
+        word = (uint32_t)(left >> 32);
+    }
+    if constexpr (sizeof(U) == 2) {
+        if (n & 1)
+            *p = (uint16_t)word;
+    } else if constexpr (sizeof(U) == 1) {
+        typedef uint16_t u16 __attribute__((aligned(1)));
+        if (n & 2) {
+            *reinterpret_cast<u16*>(p) = (uint16_t)word;
+            p += 2;
+            word >>= 16;
+        }
+        if (n & 1)
+            *p = (uint8_t)word;
+    }
+}
+
+// A whole vector stored; NT: not kept in the caches' order of use.
+template <class E, bool NT>
+__device__ inline void store_whole(typename E::T* p, const u32x4& r)
+{
+    using Vec = typename AnyVec<typename E::T>::type;
+    if constexpr (NT)
+        __builtin_nontemporal_store(r, reinterpret_cast<Vec*>(p));
+    else
+        *reinterpret_cast<Vec*>(p) = r;
+}
+
+// Elements [c, c + VEC) of a row of `cols`, as far as it goes.
+template <class E, bool NT>
+__device__ inline void store_vec(typename E::T* p, const u32x4& r, uint32_t c, uint32_t cols)
+{
+    if (c + E::VEC <= cols)
+        store_whole<E, NT>(p + c, r);
+    else if (c < cols)
+        store_head(p + c, r, cols - c);
 }
 
 // VEC float values rounded to a vector of T.
@@ -209,24 +329,37 @@ __device__ inline u32x4 narrow_slot(const float (&v)[E::VEC])
     return r;
 }
 
-// VEC weights from column c, of the stream's type or float32.
+// VEC weights from column c of `cols` >= VEC, of the stream's type or float32;
+// past the end they are zero.
 template <class E, bool WF32>
-__device__ inline void load_weight(const void* w, uint32_t c, uint32_t cols, float (&o)[E::VEC])
-{
-    if constexpr (WF32) {
+struct Weight {
+    static constexpr int N = WF32 ? E::VEC / 4 : 1;
+    using W = typename std::conditional<WF32, Elem<AR_FLOAT32>, E>::type;
+    u32x4 r[N];
+    __device__ void load(const void* w, uint32_t c, uint32_t cols)
+    {
 #pragma unroll
-        for (int h = 0; h < E::VEC / 4; ++h) {
-            float part[4];
-            widen_slot<Elem<AR_FLOAT32>, 4>(
-                load_part<Elem<AR_FLOAT32>>(static_cast<const float*>(w), c + 4 * h, cols), part);
+        for (int h = 0; h < N; ++h)
+            r[h] = load_vec<W>(static_cast<const typename W::T*>(w), c + 4 * h, cols);
+    }
+    __device__ void fit_to(uint32_t c, uint32_t cols)
+    {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int h = 0; h < N; ++h)
+            fit<W>(r[h], c + 4 * h, cols);
+    }
+    __device__ void get(float (&o)[E::VEC]) const
+    {
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+            float part[W::VEC];
+            widen_slot<W, W::VEC>(r[h], part);
+#pragma unroll
+            for (int i = 0; i < W::VEC; ++i)
                 o[4 * h + i] = part[i];
         }
-    } else {
-        widen_slot<E, E::VEC>(load_part<E>(static_cast<const typename E::T*>(w), c, cols), o);
     }
-}
+};
 
 // The weight of column c, float32 or of the stream's type.
 template <class E>

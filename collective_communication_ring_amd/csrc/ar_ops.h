@@ -39,6 +39,9 @@ struct NormArgs {
     float divisor;         // 1, or the number of ranks (average)
     float eps;
     int weight_f32;        // weight is float32 (else of the stream's type)
+    uint32_t lanes;        // threads per row (set by the launch)
+    int exact;             // lanes hold a row without a rest (set by the launch)
+    int stream;            // outputs larger than the L2s (set by the launch)
 };
 
 struct NormBackArgs {
@@ -59,17 +62,29 @@ struct NormBackArgs {
     int ranks;
     int blocks;            // partial rows of dweight per rank
     int weight_f32;
+    uint32_t lanes;        // threads per row, and rows side by side in a workgroup
+    uint32_t rows;         //   (set by the launch)
+    int exact;             // lanes hold a row without a rest (set by the launch)
+    int stream;            // dx is larger than the L2s (set by the launch)
 };
 
+constexpr int kMaxWaves = 16;                // waves that share a row, at most
 constexpr uint64_t kNormMaxCols = 1u << 30;  // 32-bit column indexes in the kernels
-constexpr int kNormBackMaxBlocks = 512;      // partial rows of dweight per rank, at most
+// Bytes of an output above which whole rows of it are stored non-temporally:
+// what the 8 L2s hold.  bf16 8192 x 8192 with e4m3 output 82 -> 75 us, bf16 4097
+// x 16384 107 -> 95 us; smaller outputs are left for whoever reads them next,
+// and rows that do not fill their last lines lose by it (2568: 33 -> 35 us).
+constexpr uint64_t kStreamBytes = (uint64_t)32 << 20;
+// Partial rows of dweight of all ranks, at most: a workgroup of 16 waves on each
+// CU, all resident (bf16 8192 x 8192: 512 of them 103 us, 256 100, 128 137).
+constexpr int kNormBackMaxBlocks = 256;
 
 // Partial rows of dweight for one rank's rows (the same for every type, so
 // that the workspace is known from sizes alone).
 int norm_back_blocks(uint64_t rows_per_rank, int ranks);
 
-hipError_t launch_rmsnorm(int dtype, bool e4m3, const NormArgs& a, hipStream_t s);
-hipError_t launch_rmsnorm_back(int dtype, const NormBackArgs& a, hipStream_t s);
+hipError_t launch_rmsnorm(int dtype, bool e4m3, NormArgs a, hipStream_t s);
+hipError_t launch_rmsnorm_back(int dtype, NormBackArgs a, hipStream_t s);
 
 // ---- gradient lists ---------------------------------------------------------
 
