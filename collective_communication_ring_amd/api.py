@@ -10,6 +10,7 @@ There is no fallback: if ``libar.so`` has not been built, ``lib()`` raises.
 """
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libar.so")
@@ -113,9 +114,10 @@ def lib():
         "ar_stream_create_cu_masked": ([ctypes.POINTER(vp), ctypes.c_uint32,
                                         ctypes.POINTER(ctypes.c_uint32)], i),
         "ar_stream_destroy": ([vp], i),
-        "ar_rmsnorm": ([ctypes.POINTER(ar_rmsnorm_t), vp], i),
-        "ar_reduce_scatter_rmsnorm": ([vp, vp, ctypes.POINTER(ar_rmsnorm_t), vp], i),
-        "ar_rmsnorm_backward": ([ctypes.POINTER(ar_rmsnorm_backward_t), vp], i),
+        # the argument structs: byref() of one, or its bytes
+        "ar_rmsnorm": ([vp, vp], i),
+        "ar_reduce_scatter_rmsnorm": ([vp, vp, vp, vp], i),
+        "ar_rmsnorm_backward": ([vp, vp], i),
         "ar_rmsnorm_backward_workspace": ([i, sz, sz], sz),
         "ar_grad_norm": ([vp, ctypes.POINTER(ar_span_t), sz, vp, vp], i),
         "ar_grad_clip": ([ctypes.POINTER(ar_span_t), ctypes.POINTER(ar_span_t), sz, vp,
@@ -266,16 +268,17 @@ def ar_stream_destroy(stream):
 
 def ar_rmsnorm(args, stream=0):
     """args: an ar_rmsnorm_t."""
-    _ok(lib().ar_rmsnorm(args, stream), "ar_rmsnorm")
+    _ok(lib().ar_rmsnorm(ctypes.byref(args), stream), "ar_rmsnorm")
 
 
 def ar_reduce_scatter_rmsnorm(comm, send_ptr, args, stream=0):
-    _ok(lib().ar_reduce_scatter_rmsnorm(comm, send_ptr, args, stream), "ar_reduce_scatter_rmsnorm")
+    _ok(lib().ar_reduce_scatter_rmsnorm(comm, send_ptr, ctypes.byref(args), stream),
+        "ar_reduce_scatter_rmsnorm")
 
 
 def ar_rmsnorm_backward(args, stream=0):
     """args: an ar_rmsnorm_backward_t."""
-    _ok(lib().ar_rmsnorm_backward(args, stream), "ar_rmsnorm_backward")
+    _ok(lib().ar_rmsnorm_backward(ctypes.byref(args), stream), "ar_rmsnorm_backward")
 
 
 def ar_rmsnorm_backward_workspace(ranks, rows, cols):
@@ -299,64 +302,100 @@ def _torch_dtype(dt):
     return {AR_INT32: torch.int32, AR_FLOAT32: torch.float32, AR_BF16: torch.bfloat16}[dt]
 
 
+_codes = {}
+
+
 def _dtype_code(dtype):
-    """AR_* of a torch dtype's name (None: not one of the library's)."""
-    return {"torch.int32": AR_INT32, "torch.float32": AR_FLOAT32, "torch.bfloat16": AR_BF16,
-            "torch.float8_e4m3fn": AR_E4M3}.get(str(dtype))
+    """AR_* of a torch dtype (None: not one of the library's)."""
+    if not _codes:
+        import torch
+        _codes.update({torch.int32: AR_INT32, torch.float32: AR_FLOAT32, torch.bfloat16: AR_BF16,
+                       torch.float8_e4m3fn: AR_E4M3})
+    return _codes.get(dtype)
 
 
-def _raw_stream(device, stream):
-    import torch
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+_current_raw_stream = None
 
 
-def _check_stream_types(x, weight, what):
-    """AR_* codes of a norm's stream and weight tensors."""
-    dt = _dtype_code(x.dtype)
-    if dt not in (AR_FLOAT32, AR_BF16):
-        raise ValueError("%s has dtype %s: float32 or bfloat16 is wanted" % (what, x.dtype))
-    wdt = _dtype_code(weight.dtype)
-    if wdt != dt and wdt != AR_FLOAT32:
-        raise ValueError("weight has dtype %s: %s or torch.float32 is wanted"
-                         % (weight.dtype, x.dtype))
-    if weight.dim() != 1 or not weight.is_contiguous():
-        raise ValueError("weight must be a contiguous vector")
-    return dt, wdt
+def _raw_stream(index, stream):
+    """The stream's handle, or that of the device's current one."""
+    global _current_raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is None:
+        import torch
+        # without the Stream object that the public call makes, where this torch has it
+        _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _current_raw_stream(index)
 
 
-def _check_like(t, device, shape, dtype, what, contiguous=False):
-    """A tensor of this device, shape and dtype whose last dimension is
-    contiguous (or all of it); returns its address, None for None."""
-    if t is None:
-        return None
-    if t.device != device:
-        raise ValueError("%s must be on %s, not %s" % (what, device, t.device))
-    if dtype is not None and t.dtype != dtype:
+def _refuse(t, index, shape, dtype, what):
+    """Says which of a tensor's properties is not the wanted one."""
+    if t.get_device() != index:
+        raise ValueError("%s must be on cuda:%d, not %s" % (what, index, t.device))
+    if t.dtype != dtype:
         raise ValueError("%s has dtype %s, not %s" % (what, t.dtype, dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, not %s" % (what, tuple(shape), tuple(t.shape)))
-    if contiguous:
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % what)
-    elif t.stride(-1) != 1 and shape[-1] > 1:
+    raise ValueError("%s must have shape %s, not %s" % (what, tuple(shape), tuple(t.shape)))
+
+
+def _rows_of(t, index, shape, dtype, what):
+    """Address and row distance of a [rows, cols] tensor on device `index`;
+    (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    if t.get_device() != index or t.dtype != dtype or t.shape != shape:
+        _refuse(t, index, shape, dtype, what)
+    row, col = t.stride()
+    if col != 1 and shape[1] > 1:
         raise ValueError("the last dimension of %s must be contiguous" % what)
+    return t.data_ptr(), row
+
+
+def _block_of(t, index, shape, dtype, what):
+    """Address of a contiguous tensor; 0 for None."""
+    if t is None:
+        return 0
+    if t.get_device() != index or t.dtype != dtype or t.shape != shape:
+        _refuse(t, index, shape, dtype, what)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
     return t.data_ptr()
 
 
-def _check_norm_outputs(x, y, scale, group, rows, cols, dtype):
-    """Output code of a norm, its groups per row, and scale's expected presence."""
+def _norm_types(x, weight, what):
+    """AR_* codes of a norm's stream and weight, and the stream's device."""
+    dt, wdt = _dtype_code(x.dtype), _dtype_code(weight.dtype)
+    if dt != AR_FLOAT32 and dt != AR_BF16:
+        raise ValueError("%s has dtype %s: float32 or bfloat16 is wanted" % (what, x.dtype))
+    if wdt != dt and wdt != AR_FLOAT32:
+        raise ValueError("weight has dtype %s: %s or torch.float32 is wanted"
+                         % (weight.dtype, x.dtype))
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("%s must be on the GPU" % what)
+    return dt, wdt, index
+
+
+def _norm_output(x, y, scale, group, cols, dt):
+    """AR_* code of a norm's output, and its scales per row."""
     out = _dtype_code(y.dtype)
-    if out != dtype and out != AR_E4M3:
-        raise ValueError("y has dtype %s: %s or torch.float8_e4m3fn is wanted" % (y.dtype, x.dtype))
-    if out != AR_E4M3:
+    if out == dt:
         if scale is not None or group:
             raise ValueError("scale and group belong to an e4m3 output")
         return out, 0
+    if out != AR_E4M3:
+        raise ValueError("y has dtype %s: %s or torch.float8_e4m3fn is wanted" % (y.dtype, x.dtype))
     if scale is None:
         raise ValueError("an e4m3 output needs scale")
     if group not in (0, 32, 64, 128, 256):
         raise ValueError("group must be 0 (a whole row), 32, 64, 128 or 256, got %r" % (group,))
     return out, -(-cols // group) if group else 1
+
+
+# the argument structs, packed in one call (native alignment, as ctypes lays them out)
+_pack_norm = struct.Struct("@iiifNNNPNPNPPNPNPP").pack
+_pack_backward = struct.Struct("@iiiNNPNPNPPPNPNPPN").pack
 
 
 def rmsnorm(x, weight, y, eps=1e-6, residual=None, sum=None, scale=None, group=0, rstd=None,
@@ -370,29 +409,29 @@ def rmsnorm(x, weight, y, eps=1e-6, residual=None, sum=None, scale=None, group=0
     group)] float32, one scale for each ``group`` (32, 64, 128, 256; 0: all)
     columns.  sum or y may be x or residual.  Asynchronous on the current
     torch stream (or the given one)."""
-    if x.dim() != 2:
-        raise ValueError("x must have shape (rows, cols), got %s" % (tuple(x.shape),))
     shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("x must have shape (rows, cols), got %s" % (tuple(shape),))
     rows, cols = shape
-    dt, wdt = _check_stream_types(x, weight, "x")
-    out, groups = _check_norm_outputs(x, y, scale, group, rows, cols, dt)
-    dev = x.device
-    if not x.is_cuda:
-        raise ValueError("x must be on the GPU")
-    import torch
-    f32 = torch.float32
-    args = ar_rmsnorm_t(
+    dtype, f32 = x.dtype, _f32()
+    dt, wdt, dev = _norm_types(x, weight, "x")
+    out, groups = _norm_output(x, y, scale, group, cols, dt)
+    rc = (_lib or lib()).ar_rmsnorm(_pack_norm(
         dt, out, wdt, eps, rows, cols, group,
-        _check_like(x, dev, shape, None, "x"), x.stride(0),
-        _check_like(residual, dev, shape, x.dtype, "residual"),
-        residual.stride(0) if residual is not None else 0,
-        _check_like(weight, dev, shape[1:], None, "weight"),
-        _check_like(sum, dev, shape, x.dtype, "sum"), sum.stride(0) if sum is not None else 0,
-        _check_like(y, dev, shape, None, "y"), y.stride(0),
-        _check_like(scale, dev, (rows, groups), f32, "scale", True),
-        _check_like(rstd, dev, shape[:1], f32, "rstd", True))
-    ar_rmsnorm(args, _raw_stream(dev, stream))
+        *_rows_of(x, dev, shape, dtype, "x"), *_rows_of(residual, dev, shape, dtype, "residual"),
+        _block_of(weight, dev, (cols,), weight.dtype, "weight"),
+        *_rows_of(sum, dev, shape, dtype, "sum"), *_rows_of(y, dev, shape, y.dtype, "y"),
+        _block_of(scale, dev, (rows, groups), f32, "scale"),
+        _block_of(rstd, dev, (rows,), f32, "rstd")),
+        _raw_stream(dev, stream))
+    if rc:
+        raise ArError(rc, "ar_rmsnorm")
     return y
+
+
+def _f32():
+    import torch
+    return torch.float32
 
 
 def rmsnorm_backward_workspace(ranks, rows, cols, device="cuda"):
@@ -410,36 +449,31 @@ def rmsnorm_backward(dy, x, weight, rstd, dx, dweight, dsum=None, workspace=None
     sum from elsewhere; dweight is [ranks, cols] float32, a row for each of
     ``ranks`` equal shards of the rows.  dx may be dy, x or dsum.  Without
     ``workspace`` (``rmsnorm_backward_workspace``) one is allocated."""
-    if x.dim() != 2 or dweight.dim() != 2:
-        raise ValueError("x must have shape (rows, cols) and dweight (ranks, cols)")
-    import torch
     shape = x.shape
+    if len(shape) != 2 or dweight.dim() != 2:
+        raise ValueError("x must have shape (rows, cols) and dweight (ranks, cols)")
     rows, cols = shape
     ranks = dweight.shape[0]
-    dt, wdt = _check_stream_types(x, weight, "x")
-    dev = x.device
-    if not x.is_cuda:
-        raise ValueError("x must be on the GPU")
+    dtype, f32 = x.dtype, _f32()
+    dt, wdt, dev = _norm_types(x, weight, "x")
     if ranks < 1 or rows % ranks:
         raise ValueError("%d rows are not %d equal shards" % (rows, ranks))
     if workspace is None:
-        workspace = rmsnorm_backward_workspace(ranks, rows, cols, dev)
+        workspace = rmsnorm_backward_workspace(ranks, rows, cols, x.device)
         if stream is not None:
             workspace.record_stream(stream)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
-    f32 = torch.float32
-    args = ar_rmsnorm_backward_t(
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on cuda:%d" % dev)
+    rc = (_lib or lib()).ar_rmsnorm_backward(_pack_backward(
         dt, wdt, ranks, rows, cols,
-        _check_like(dy, dev, shape, x.dtype, "dy"), dy.stride(0),
-        _check_like(x, dev, shape, None, "x"), x.stride(0),
-        _check_like(weight, dev, shape[1:], None, "weight"),
-        _check_like(rstd, dev, shape[:1], f32, "rstd", True),
-        _check_like(dsum, dev, shape, x.dtype, "dsum"), dsum.stride(0) if dsum is not None else 0,
-        _check_like(dx, dev, shape, x.dtype, "dx"), dx.stride(0),
-        _check_like(dweight, dev, (ranks, cols), f32, "dweight", True),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    ar_rmsnorm_backward(args, _raw_stream(dev, stream))
+        *_rows_of(dy, dev, shape, dtype, "dy"), *_rows_of(x, dev, shape, dtype, "x"),
+        _block_of(weight, dev, (cols,), weight.dtype, "weight"),
+        _block_of(rstd, dev, (rows,), f32, "rstd"),
+        *_rows_of(dsum, dev, shape, dtype, "dsum"), *_rows_of(dx, dev, shape, dtype, "dx"),
+        _block_of(dweight, dev, (ranks, cols), f32, "dweight"),
+        workspace.data_ptr(), workspace.nbytes), _raw_stream(dev, stream))
+    if rc:
+        raise ArError(rc, "ar_rmsnorm_backward")
     return dx
 
 
@@ -465,30 +499,35 @@ class TensorList:
     that has changed (``t.data`` was set) is taken up by the next call."""
 
     def __init__(self, tensors):
+        import torch
         self.tensors = list(tensors)
-        self.device = self.tensors[0].device if self.tensors else None
+        self._address = torch.Tensor.data_ptr
         self._array = (ar_span_t * len(self.tensors))()
         self._fill()
 
     def _fill(self):
-        for i, t in enumerate(self.tensors):
+        ts = self.tensors
+        self.index = ts[0].get_device() if ts else None  # the GPU's
+        spans = []
+        for i, t in enumerate(ts):
             dt = _dtype_code(t.dtype)
-            if dt not in (AR_FLOAT32, AR_BF16):
+            if dt != AR_FLOAT32 and dt != AR_BF16:
                 raise ValueError("tensor %d has dtype %s: float32 or bfloat16 is wanted" % (i, t.dtype))
-            if t.device != self.device or not t.is_cuda:
+            if t.get_device() != self.index or self.index < 0:
                 raise ValueError("tensor %d is on %s: all must be on one GPU" % (i, t.device))
             if not _dense(t):
                 raise ValueError("tensor %d is not dense in memory" % i)
-            self._array[i] = ar_span_t(t.data_ptr(), t.numel(), dt)
-        self._ptrs = [t.data_ptr() for t in self.tensors]
+            spans += (t.data_ptr(), t.numel(), dt)
+        struct.pack_into("@" + "PNi0P" * len(ts), self._array, 0, *spans)
+        self._ptrs = list(map(self._address, ts))
         # element for element: an output needs its input's type and layout
-        self._layout = [(t.dtype, t.shape, t.stride()) for t in self.tensors]
+        self._layout = [(t.dtype, t.shape, t.stride()) for t in ts]
 
     def __len__(self):
         return len(self.tensors)
 
     def spans(self):
-        if [t.data_ptr() for t in self.tensors] != self._ptrs:
+        if list(map(self._address, self.tensors)) != self._ptrs:
             self._fill()
         return self._array
 
@@ -527,6 +566,10 @@ class Comm:
                          self._stream(None))
 
     def _stream(self, stream):
+        if stream is None and self.workspace is not None:
+            raw = _raw_stream(self.workspace.get_device(), None)
+            if raw == self._ws_stream:
+                return raw
         import torch
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
         if getattr(self, "workspace", None) is not None and \
@@ -574,26 +617,28 @@ class Comm:
         of residual, sum and y ([R, tokens * cols]) holds its own tokens;
         weight [cols] gives the row length; rstd is [R, tokens] and scale
         [R, tokens * ceil(cols / group)].  Otherwise as ``rmsnorm``."""
-        import torch
         cols = weight.shape[0] if weight.dim() == 1 else 0
-        if y.dim() != 2 or y.shape[0] != self.R or (cols and y.shape[1] % cols):
+        shape = y.shape
+        if len(shape) != 2 or shape[0] != self.R or (cols and shape[1] % cols):
             raise ValueError("y must have shape (%d, tokens * %d), got %s"
-                             % (self.R, cols, tuple(y.shape)))
-        n = y.shape[1]
+                             % (self.R, cols, tuple(shape)))
+        R, n = shape
         tokens = n // cols if cols else 0
-        self._check_tensor(send, self.R, n * self.R, "send")
-        dt, wdt = _check_stream_types(send, weight, "send")
-        out, groups = _check_norm_outputs(send, y, scale, group, tokens, cols, dt)
-        dev, shape, f32 = send.device, (self.R, n), torch.float32
-        args = ar_rmsnorm_t(
-            dt, out, wdt, eps, tokens, cols, group, None, 0,
-            _check_like(residual, dev, shape, send.dtype, "residual", True), 0,
-            _check_like(weight, dev, (cols,), None, "weight"),
-            _check_like(sum, dev, shape, send.dtype, "sum", True), 0,
-            _check_like(y, dev, shape, None, "y", True), 0,
-            _check_like(scale, dev, (self.R, tokens * groups), f32, "scale", True),
-            _check_like(rstd, dev, (self.R, tokens), f32, "rstd", True))
-        ar_reduce_scatter_rmsnorm(self.handle, send.data_ptr(), args, self._stream(stream))
+        self._check_tensor(send, R, n * R, "send")
+        dtype, f32 = send.dtype, _f32()
+        dt, wdt, dev = _norm_types(send, weight, "send")
+        out, groups = _norm_output(send, y, scale, group, cols, dt)
+        rc = (_lib or lib()).ar_reduce_scatter_rmsnorm(
+            self.handle, send.data_ptr(), _pack_norm(
+                dt, out, wdt, eps, tokens, cols, group, 0, 0,
+                _block_of(residual, dev, shape, dtype, "residual"), 0,
+                _block_of(weight, dev, (cols,), weight.dtype, "weight"),
+                _block_of(sum, dev, shape, dtype, "sum"), 0,
+                _block_of(y, dev, shape, y.dtype, "y"), 0,
+                _block_of(scale, dev, (R, tokens * groups), f32, "scale"),
+                _block_of(rstd, dev, (R, tokens), f32, "rstd")), self._stream(stream))
+        if rc:
+            raise ArError(rc, "ar_reduce_scatter_rmsnorm")
         return y
 
     def grad_norm(self, grads, norm, stream=None):
@@ -602,8 +647,9 @@ class Comm:
         device (``ar_grad_norm``).  Uses the comm's workspace: ordered with its
         collectives on one stream."""
         grads = _tensor_list(grads)
+        spans = grads.spans()
         self._check_norm(grads, norm)
-        ar_grad_norm(self.handle, grads.spans(), len(grads), norm.data_ptr(), self._stream(stream))
+        ar_grad_norm(self.handle, spans, len(grads), norm.data_ptr(), self._stream(stream))
         return norm
 
     def grad_clip(self, grads, norm, max_norm, out=None, stream=None):
@@ -611,18 +657,20 @@ class Comm:
         ``norm`` being theirs on the device (``ar_grad_clip``): in place, or
         into the tensors of ``out``."""
         grads = _tensor_list(grads)
-        out = grads if out is None else _tensor_list(out)
+        spans = grads.spans()
         self._check_norm(grads, norm)
-        if out is not grads and (out._layout != grads._layout or out.device != grads.device):
-            raise ValueError("out must have the shapes, dtypes, strides and device of grads")
-        ar_grad_clip(grads.spans(), grads.spans() if out is grads else out.spans(), len(grads),
-                     norm.data_ptr(), max_norm, self._stream(stream))
+        to = spans
+        if out is not None:
+            out = _tensor_list(out)
+            to = out.spans()
+            if out._layout != grads._layout or out.index != grads.index:
+                raise ValueError("out must have the shapes, dtypes, strides and device of grads")
+        ar_grad_clip(spans, to, len(grads), norm.data_ptr(), max_norm, self._stream(stream))
         return norm
 
     def _check_norm(self, grads, norm):
-        import torch
-        if norm.numel() != 1 or norm.dtype != torch.float32 or not norm.is_cuda or \
-                (grads.device is not None and grads.device != norm.device):
+        if norm.numel() != 1 or norm.dtype != _f32() or not norm.is_cuda or \
+                (grads.index is not None and grads.index != norm.get_device()):
             raise ValueError("norm must be one float32 on the gradients' device")
 
     def check(self):

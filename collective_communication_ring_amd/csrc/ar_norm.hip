@@ -147,8 +147,8 @@ __global__ __launch_bounds__(MAXT) void k_norm(NormArgs a)
     __shared__ uint32_t s_u[kMaxWaves];
     const uint32_t lanes = a.lanes, wave = threadIdx.x >> 6;
     const uint32_t lane = lanes <= 64 ? threadIdx.x & (lanes - 1) : threadIdx.x;
-    const uint64_t t = lanes <= 64 ? ((uint64_t)blockIdx.x * blockDim.x + threadIdx.x) / lanes
-                                   : blockIdx.x;
+    const uint64_t t = a.row0 + (lanes <= 64 ? (blockIdx.x * blockDim.x + threadIdx.x) / lanes
+                                             : blockIdx.x);
     if (t >= a.rows)  // all threads of a row; rows of several waves have no such workgroup
         return;
     const auto column = [&](int k) { return (k * lanes + lane) * V; };
@@ -326,17 +326,20 @@ void launch_row(NormArgs a, uint32_t nvec, hipStream_t s)
             a.lanes /= 2;
     a.exact = a.cols == NV * a.lanes * E::VEC;
     const uint32_t rows = a.lanes <= 64 ? kBlock / a.lanes : 1;
-    hipLaunchKernelGGL((k_norm<E, WF32, Q, NV, MULTI, MAXT>),
-                       dim3((unsigned)((a.rows + rows - 1) / rows)), dim3(a.lanes * rows), 0, s, a);
+    const uint64_t most = kNormMaxThreads / a.lanes;  // a multiple of a workgroup's rows
+    for (a.row0 = 0; a.row0 < a.rows; a.row0 += most) {
+        const uint64_t n = std::min<uint64_t>(a.rows - a.row0, most);
+        hipLaunchKernelGGL((k_norm<E, WF32, Q, NV, MULTI, MAXT>), dim3((unsigned)((n + rows - 1) / rows)),
+                           dim3(a.lanes * rows), 0, s, a);
+    }
 }
 
 template <class E, bool WF32, bool Q, bool MULTI>
 void launch_typed(const NormArgs& a, hipStream_t s)
 {
     const uint32_t nvec = (a.cols + E::VEC - 1) / E::VEC;
-    // rows of less than a vector, of more than 4096, and more rows than a grid
-    // holds go an element at a time
-    if (a.cols < E::VEC || nvec > 64 * 4 * kMaxWaves || a.rows > 1u << 30)
+    // rows of less than a vector and of more than 4096 go an element at a time
+    if (a.cols < E::VEC || nvec > 64 * 4 * kMaxWaves)
         hipLaunchKernelGGL((k_norm_any<E, Q>), dim3((unsigned)std::min<uint64_t>(a.rows, 1u << 16)),
                            dim3(kBlock), 0, s, a);
     else if (nvec > 64 * 2 * kMaxWaves)

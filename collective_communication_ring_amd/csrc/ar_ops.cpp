@@ -283,36 +283,50 @@ int grid_for(uint32_t tiles)
     return (int)std::max<uint32_t>(1, std::min<uint32_t>(tiles, kGradMaxBlocks));
 }
 
-// An output may be written while nothing else reads or writes its bytes.
+// A stretch of addresses.
 struct Reach {
     uintptr_t lo, hi;
-    bool write;
 };
 
+bool before(const Reach& x, const Reach& y) { return x.lo < y.lo; }
+
+void sort_reaches(std::vector<Reach>* v)
+{
+    // tensors cut from one buffer come in order
+    if (!std::is_sorted(v->begin(), v->end(), before))
+        std::sort(v->begin(), v->end(), before);
+}
+
+// Whether an output shares bytes with another output, or with an input that is
+// not its own in place.
 bool clip_overlaps(const ar_span_t* in, const ar_span_t* out, size_t n, const float* norm)
 {
-    std::vector<Reach> v;
-    v.reserve(2 * n + 1);
+    std::vector<Reach> reads, writes;
+    reads.reserve(n + 1);
+    writes.reserve(n);
     for (size_t i = 0; i < n; ++i) {
         const size_t bytes = in[i].count * size_of(in[i].dtype);
         if (!bytes)
             continue;
         const uintptr_t a = (uintptr_t)in[i].data, b = (uintptr_t)out[i].data;
         if (a != b)
-            v.push_back({a, a + bytes, false});
-        v.push_back({b, b + bytes, true});
+            reads.push_back({a, a + bytes});
+        writes.push_back({b, b + bytes});
     }
-    v.push_back({(uintptr_t)norm, (uintptr_t)norm + 4, false});
-    const auto before = [](const Reach& x, const Reach& y) { return x.lo < y.lo; };
-    if (!std::is_sorted(v.begin(), v.end(), before))
-        std::sort(v.begin(), v.end(), before);
-    uintptr_t end_any = 0, end_write = 0;
-    for (const Reach& r : v) {
-        if (r.lo < (r.write ? end_any : end_write))
+    reads.push_back({(uintptr_t)norm, (uintptr_t)norm + sizeof(float)});
+    sort_reaches(&reads);
+    sort_reaches(&writes);
+    for (size_t k = 1; k < writes.size(); ++k)
+        if (writes[k].lo < writes[k - 1].hi)
             return true;
-        end_any = std::max(end_any, r.hi);
-        if (r.write)
-            end_write = std::max(end_write, r.hi);
+    // the writes are disjoint now, so their ends are in order too: for a read,
+    // the first that ends behind its start is the only one to look at
+    auto w = writes.begin();
+    for (const Reach& r : reads) {
+        while (w != writes.end() && w->hi <= r.lo)
+            ++w;
+        if (w != writes.end() && w->lo < r.hi)
+            return true;
     }
     return false;
 }

@@ -25,6 +25,7 @@ struct NormArgs {
     void* y;
     float* scale;          // e4m3 only: [rows][groups]
     float* rstd;           // or NULL
+    uint64_t row0;         // this launch's first row (set by the launch)
     uint64_t rows;
     uint64_t x_stride;
     uint64_t res_stride;
@@ -69,7 +70,10 @@ struct NormBackArgs {
 };
 
 constexpr int kMaxWaves = 16;                // waves that share a row, at most
-constexpr uint64_t kNormMaxCols = 1u << 30;  // 32-bit column indexes in the kernels
+constexpr uint64_t kNormMaxCols = 1u << 28;  // 32-bit column and thread numbers in a launch
+// Threads of a launch of the forward norm, at most (a grid holds fewer than
+// 2^32): more rows go by several launches.
+constexpr uint64_t kNormMaxThreads = (uint64_t)1 << 31;
 // Bytes of an output above which whole rows of it are stored non-temporally:
 // what the 8 L2s hold.  bf16 8192 x 8192 with e4m3 output 82 -> 75 us, bf16 4097
 // x 16384 107 -> 95 us; smaller outputs are left for whoever reads them next,

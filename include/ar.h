@@ -414,7 +414,7 @@ int ar_ll_pingpong(void* lines, uint32_t* result_dev, int iters, int xcd_apart,
  * output may share x's or residual's array, with the same address, stride and
  * type; any other overlap of an output is AR_ERR_INVALID_USAGE (rows
  * interleaved in one array with one stride do not overlap).
- * rows == 0 or cols == 0 is a successful no-op.  cols is at most 2^30. */
+ * rows == 0 or cols == 0 is a successful no-op.  cols is at most 2^28. */
 typedef struct {
     int dtype;        /* AR_FLOAT32 or AR_BF16: x, residual, sum */
     int out_dtype;    /* y: dtype, or AR_E4M3 */

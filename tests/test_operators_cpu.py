@@ -41,7 +41,7 @@ def _norm(api, **change):
     dict(x=None), dict(weight=None), dict(y=None),
     dict(x_stride=99), dict(residual_stride=3), dict(sum_stride=0), dict(y_stride=99),
     dict(x=X + 1), dict(residual=RES + 1), dict(sum=SUM + 1), dict(y=Y + 1), dict(weight=W + 1),
-    dict(rstd=RSTD + 2), dict(cols=(1 << 30) + 1, x_stride=1 << 31), dict(x_stride=1 << 45),
+    dict(rstd=RSTD + 2), dict(cols=(1 << 28) + 1, x_stride=1 << 31), dict(x_stride=1 << 45),
     dict(rows=1 << 60), dict(rows=(1 << 64) - 1),
     dict(out_dtype=3), dict(out_dtype=3, scale=SCALE + 2),
     dict(out_dtype=3, scale=SCALE, group=16), dict(out_dtype=3, scale=SCALE, group=100),
@@ -124,7 +124,7 @@ def _back(api, **change):
     dict(dy=None), dict(x=None), dict(weight=None), dict(rstd=None), dict(dx=None),
     dict(dweight=None), dict(workspace=None), dict(workspace=WS + 64), dict(workspace_bytes=255),
     dict(dy_stride=49), dict(x_stride=49), dict(dsum_stride=49), dict(dx_stride=49),
-    dict(dx=DX + 2), dict(rstd=BR + 1), dict(dweight=DW + 2), dict(cols=(1 << 30) + 1),
+    dict(dx=DX + 2), dict(rstd=BR + 1), dict(dweight=DW + 2), dict(cols=(1 << 28) + 1),
     dict(rows=(1 << 63)), dict(dx_stride=1 << 60),
 ])
 def test_backward_refuses_bad_arguments(api, change):
@@ -202,6 +202,34 @@ def test_grad_clip_refusals(api):
     twice = _spans(api, (X, 10, F), (X, 10, F))
     assert call(twice, twice, 2) == usage
     assert call(one, one, 1, norm=X + 8) == usage
+
+
+def test_packed_arguments_match_the_structs(api):
+    """The wrappers pack their arguments in one call: the same bytes as the
+    structs hold field by field (the same sizes, types and order)."""
+    import struct
+    codes = {ctypes.c_int: "i", ctypes.c_float: "f", ctypes.c_size_t: "N", ctypes.c_void_p: "P"}
+    for cls, pack in ((api.ar_rmsnorm_t, api._pack_norm),
+                      (api.ar_rmsnorm_backward_t, api._pack_backward)):
+        a = cls()
+        values = [float(k) if t is ctypes.c_float else k for k, (_, t) in enumerate(cls._fields_, 1)]
+        for v, (name, _) in zip(values, cls._fields_):
+            setattr(a, name, v)
+        want = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_))
+        assert want.size == ctypes.sizeof(cls)
+        assert pack(*values) == want.pack(*values) == bytes(a)
+
+
+def test_struct_fields_match_the_header(api):
+    """The ctypes structs list the header's fields, in order."""
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(root, "include", "ar.h")).read(), flags=re.S)
+    for cls in (api.ar_rmsnorm_t, api.ar_rmsnorm_backward_t, api.ar_span_t):
+        body = re.search(r"typedef struct \{([^{}]*)\} %s;" % cls.__name__, src).group(1)
+        names = [n.strip().lstrip("* ") for decl in body.split(";") if decl.strip()
+                 for n in re.sub(r"^\s*(const\s+)?\w+\s*", "", decl.strip()).split(",")]
+        assert names == [n for n, _ in cls._fields_], cls.__name__
 
 
 def test_tensor_list_checks(api):

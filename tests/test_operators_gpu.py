@@ -213,6 +213,25 @@ def test_norm_rows_past_32_bits(env):
     ob.between(x, *form["sum"], "sum")
 
 
+def test_norm_of_more_rows_than_a_launch_holds(env):
+    """2^26 + 5 rows of 64 lanes each are past 2^32 threads: 35 GB of rows, by
+    three launches; rows on both sides of their borders are checked."""
+    torch, api, dev = env["torch"], env["api"], env["dev"]
+    rows, cols = (1 << 26) + 5, 264
+    at = sorted({0, 1, (1 << 25) - 1, 1 << 25, (1 << 25) + 3, (1 << 26) - 1, 1 << 26, rows - 1})
+    hx = _rand(env, (len(at), cols), 1, torch.bfloat16)
+    x = torch.ones((rows, cols), dtype=torch.bfloat16, device=dev)
+    x[at] = hx.to(dev)
+    w = torch.ones(cols, device=dev)
+    y = torch.zeros_like(x)
+    api.rmsnorm(x, w, y, EPS)
+    torch.cuda.synchronize()
+    ob.between(y[at], *ob.norm(hx, w.cpu(), EPS)["y"], "y")
+    some = torch.arange(7, rows, 65537, device=dev)  # the rows of ones: 1 / sqrt(1 + eps) is 1
+    some = some[~torch.isin(some, torch.tensor(at, device=dev))]
+    assert (y[some] == 1).all()
+
+
 # ---- behind a reduce-scatter --------------------------------------------------
 
 @pytest.mark.parametrize("R,tokens,cols,dtype,out,group,residual,redop", [
