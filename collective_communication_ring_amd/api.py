@@ -1,16 +1,18 @@
 """Python binding of libar (C ABI declared in include/ar.h).
 
-Argument marshalling only: every step of the collective runs in libar's HIP
-kernels.  The low-level functions carry the C names (``ar_init``,
+Argument marshalling only: every step of the collectives and operators runs in
+libar's HIP kernels.  The low-level functions carry the C names (``ar_init``,
 ``ar_allreduce``, ...) and take plain integers (device pointers, sizes,
 stream handles).  ``Comm`` is a convenience wrapper over torch tensors:
 PyTorch provides device memory and streams, nothing else.
 
-There is no fallback: if ``libar.so`` has not been built, ``lib()`` raises.
+The operators' torch wrappers marshal in C++ (``_binding.so``).
+
+There is no fallback: if ``libar.so`` has not been built, ``lib()`` raises, and
+so does ``binding()`` without ``_binding.so``.
 """
 import ctypes
 import os
-import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libar.so")
@@ -114,10 +116,9 @@ def lib():
         "ar_stream_create_cu_masked": ([ctypes.POINTER(vp), ctypes.c_uint32,
                                         ctypes.POINTER(ctypes.c_uint32)], i),
         "ar_stream_destroy": ([vp], i),
-        # the argument structs: byref() of one, or its bytes
-        "ar_rmsnorm": ([vp, vp], i),
-        "ar_reduce_scatter_rmsnorm": ([vp, vp, vp, vp], i),
-        "ar_rmsnorm_backward": ([vp, vp], i),
+        "ar_rmsnorm": ([ctypes.POINTER(ar_rmsnorm_t), vp], i),
+        "ar_reduce_scatter_rmsnorm": ([vp, vp, ctypes.POINTER(ar_rmsnorm_t), vp], i),
+        "ar_rmsnorm_backward": ([ctypes.POINTER(ar_rmsnorm_backward_t), vp], i),
         "ar_rmsnorm_backward_workspace": ([i, sz, sz], sz),
         "ar_grad_norm": ([vp, ctypes.POINTER(ar_span_t), sz, vp, vp], i),
         "ar_grad_clip": ([ctypes.POINTER(ar_span_t), ctypes.POINTER(ar_span_t), sz, vp,
@@ -302,26 +303,32 @@ def _torch_dtype(dt):
     return {AR_INT32: torch.int32, AR_FLOAT32: torch.float32, AR_BF16: torch.bfloat16}[dt]
 
 
-_codes = {}
+_bound = None  # the marshalling module, and the library whose entry points it has
 
 
-def _dtype_code(dtype):
-    """AR_* of a torch dtype (None: not one of the library's)."""
-    if not _codes:
-        import torch
-        _codes.update({torch.int32: AR_INT32, torch.float32: AR_FLOAT32, torch.bfloat16: AR_BF16,
-                       torch.float8_e4m3fn: AR_E4M3})
-    return _codes.get(dtype)
+def binding():
+    """The operators' argument marshalling (_binding.so), calling lib()'s
+    entry points; raises if it is not built."""
+    global _bound
+    L = lib()
+    if _bound is not None and _bound[1] is L:
+        return _bound[0]
+    import torch  # noqa: F401  (its libraries come first)
+    if not os.path.exists(os.path.join(HERE, "_binding.so")):
+        raise RuntimeError("_binding.so is not built (in %s); run __graft_entry__.build()" % HERE)
+    from . import _binding
+    _binding.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                    (L.ar_rmsnorm, L.ar_reduce_scatter_rmsnorm, L.ar_rmsnorm_backward)))
+    _bound = (_binding, L)
+    return _binding
 
 
 _current_raw_stream = None
 
 
-def _raw_stream(index, stream):
-    """The stream's handle, or that of the device's current one."""
+def _raw_stream(index):
+    """The handle of a device's current stream."""
     global _current_raw_stream
-    if stream is not None:
-        return stream.cuda_stream
     if _current_raw_stream is None:
         import torch
         # without the Stream object that the public call makes, where this torch has it
@@ -330,72 +337,11 @@ def _raw_stream(index, stream):
     return _current_raw_stream(index)
 
 
-def _refuse(t, index, shape, dtype, what):
-    """Says which of a tensor's properties is not the wanted one."""
-    if t.get_device() != index:
-        raise ValueError("%s must be on cuda:%d, not %s" % (what, index, t.device))
-    if t.dtype != dtype:
-        raise ValueError("%s has dtype %s, not %s" % (what, t.dtype, dtype))
-    raise ValueError("%s must have shape %s, not %s" % (what, tuple(shape), tuple(t.shape)))
-
-
-def _rows_of(t, index, shape, dtype, what):
-    """Address and row distance of a [rows, cols] tensor on device `index`;
-    (0, 0) for None."""
-    if t is None:
-        return 0, 0
-    if t.get_device() != index or t.dtype != dtype or t.shape != shape:
-        _refuse(t, index, shape, dtype, what)
-    row, col = t.stride()
-    if col != 1 and shape[1] > 1:
-        raise ValueError("the last dimension of %s must be contiguous" % what)
-    return t.data_ptr(), row
-
-
-def _block_of(t, index, shape, dtype, what):
-    """Address of a contiguous tensor; 0 for None."""
-    if t is None:
-        return 0
-    if t.get_device() != index or t.dtype != dtype or t.shape != shape:
-        _refuse(t, index, shape, dtype, what)
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-    return t.data_ptr()
-
-
-def _norm_types(x, weight, what):
-    """AR_* codes of a norm's stream and weight, and the stream's device."""
-    dt, wdt = _dtype_code(x.dtype), _dtype_code(weight.dtype)
-    if dt != AR_FLOAT32 and dt != AR_BF16:
-        raise ValueError("%s has dtype %s: float32 or bfloat16 is wanted" % (what, x.dtype))
-    if wdt != dt and wdt != AR_FLOAT32:
-        raise ValueError("weight has dtype %s: %s or torch.float32 is wanted"
-                         % (weight.dtype, x.dtype))
-    index = x.get_device()
-    if index < 0:
-        raise ValueError("%s must be on the GPU" % what)
-    return dt, wdt, index
-
-
-def _norm_output(x, y, scale, group, cols, dt):
-    """AR_* code of a norm's output, and its scales per row."""
-    out = _dtype_code(y.dtype)
-    if out == dt:
-        if scale is not None or group:
-            raise ValueError("scale and group belong to an e4m3 output")
-        return out, 0
-    if out != AR_E4M3:
-        raise ValueError("y has dtype %s: %s or torch.float8_e4m3fn is wanted" % (y.dtype, x.dtype))
-    if scale is None:
-        raise ValueError("an e4m3 output needs scale")
-    if group not in (0, 32, 64, 128, 256):
-        raise ValueError("group must be 0 (a whole row), 32, 64, 128 or 256, got %r" % (group,))
-    return out, -(-cols // group) if group else 1
-
-
-# the argument structs, packed in one call (native alignment, as ctypes lays them out)
-_pack_norm = struct.Struct("@iiifNNNPNPNPPNPNPP").pack
-_pack_backward = struct.Struct("@iiiNNPNPNPPPNPNPPN").pack
+def _stream_of(t, stream):
+    """The given stream's handle, or that of the current one on t's GPU."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(t.get_device()) if t.is_cuda else None
 
 
 def rmsnorm(x, weight, y, eps=1e-6, residual=None, sum=None, scale=None, group=0, rstd=None,
@@ -409,29 +355,11 @@ def rmsnorm(x, weight, y, eps=1e-6, residual=None, sum=None, scale=None, group=0
     group)] float32, one scale for each ``group`` (32, 64, 128, 256; 0: all)
     columns.  sum or y may be x or residual.  Asynchronous on the current
     torch stream (or the given one)."""
-    shape = x.shape
-    if len(shape) != 2:
-        raise ValueError("x must have shape (rows, cols), got %s" % (tuple(shape),))
-    rows, cols = shape
-    dtype, f32 = x.dtype, _f32()
-    dt, wdt, dev = _norm_types(x, weight, "x")
-    out, groups = _norm_output(x, y, scale, group, cols, dt)
-    rc = (_lib or lib()).ar_rmsnorm(_pack_norm(
-        dt, out, wdt, eps, rows, cols, group,
-        *_rows_of(x, dev, shape, dtype, "x"), *_rows_of(residual, dev, shape, dtype, "residual"),
-        _block_of(weight, dev, (cols,), weight.dtype, "weight"),
-        *_rows_of(sum, dev, shape, dtype, "sum"), *_rows_of(y, dev, shape, y.dtype, "y"),
-        _block_of(scale, dev, (rows, groups), f32, "scale"),
-        _block_of(rstd, dev, (rows,), f32, "rstd")),
-        _raw_stream(dev, stream))
+    rc = (_bound and _bound[0] or binding()).rmsnorm(
+        x, weight, y, eps, residual, sum, scale, group, rstd, _stream_of(x, stream))
     if rc:
         raise ArError(rc, "ar_rmsnorm")
     return y
-
-
-def _f32():
-    import torch
-    return torch.float32
 
 
 def rmsnorm_backward_workspace(ranks, rows, cols, device="cuda"):
@@ -449,86 +377,36 @@ def rmsnorm_backward(dy, x, weight, rstd, dx, dweight, dsum=None, workspace=None
     sum from elsewhere; dweight is [ranks, cols] float32, a row for each of
     ``ranks`` equal shards of the rows.  dx may be dy, x or dsum.  Without
     ``workspace`` (``rmsnorm_backward_workspace``) one is allocated."""
-    shape = x.shape
-    if len(shape) != 2 or dweight.dim() != 2:
-        raise ValueError("x must have shape (rows, cols) and dweight (ranks, cols)")
-    rows, cols = shape
-    ranks = dweight.shape[0]
-    dtype, f32 = x.dtype, _f32()
-    dt, wdt, dev = _norm_types(x, weight, "x")
-    if ranks < 1 or rows % ranks:
-        raise ValueError("%d rows are not %d equal shards" % (rows, ranks))
     if workspace is None:
-        workspace = rmsnorm_backward_workspace(ranks, rows, cols, x.device)
+        workspace = rmsnorm_backward_workspace(
+            dweight.shape[0], x.shape[0], x.shape[-1], x.device)
         if stream is not None:
             workspace.record_stream(stream)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on cuda:%d" % dev)
-    rc = (_lib or lib()).ar_rmsnorm_backward(_pack_backward(
-        dt, wdt, ranks, rows, cols,
-        *_rows_of(dy, dev, shape, dtype, "dy"), *_rows_of(x, dev, shape, dtype, "x"),
-        _block_of(weight, dev, (cols,), weight.dtype, "weight"),
-        _block_of(rstd, dev, (rows,), f32, "rstd"),
-        *_rows_of(dsum, dev, shape, dtype, "dsum"), *_rows_of(dx, dev, shape, dtype, "dx"),
-        _block_of(dweight, dev, (ranks, cols), f32, "dweight"),
-        workspace.data_ptr(), workspace.nbytes), _raw_stream(dev, stream))
+    rc = (_bound and _bound[0] or binding()).rmsnorm_backward(
+        dy, x, weight, rstd, dx, dweight, dsum, workspace, _stream_of(x, stream))
     if rc:
         raise ArError(rc, "ar_rmsnorm_backward")
     return dx
 
 
-def _dense(t):
-    """Whether a tensor's elements fill one block of memory, in any order of
-    its dimensions."""
-    if t.is_contiguous():
-        return True
-    want = 1
-    for stride, size in sorted(zip(t.stride(), t.shape)):
-        if size == 1:
-            continue
-        if stride != want:
-            return False
-        want *= size
-    return True
-
-
 class TensorList:
     """Gradient tensors of one GPU as ``Comm.grad_norm`` / ``Comm.grad_clip``
-    take them: float32 or bfloat16, each dense in memory.  Keeps the tensors,
-    and their addresses in a form that a call need not build again; an address
-    that has changed (``t.data`` was set) is taken up by the next call."""
+    take them: float32 or bfloat16, each dense in memory (in any order of its
+    dimensions).  Keeps the tensors; each call reads their addresses anew."""
 
     def __init__(self, tensors):
-        import torch
         self.tensors = list(tensors)
-        self._address = torch.Tensor.data_ptr
         self._array = (ar_span_t * len(self.tensors))()
-        self._fill()
-
-    def _fill(self):
-        ts = self.tensors
-        self.index = ts[0].get_device() if ts else None  # the GPU's
-        spans = []
-        for i, t in enumerate(ts):
-            dt = _dtype_code(t.dtype)
-            if dt != AR_FLOAT32 and dt != AR_BF16:
-                raise ValueError("tensor %d has dtype %s: float32 or bfloat16 is wanted" % (i, t.dtype))
-            if t.get_device() != self.index or self.index < 0:
-                raise ValueError("tensor %d is on %s: all must be on one GPU" % (i, t.device))
-            if not _dense(t):
-                raise ValueError("tensor %d is not dense in memory" % i)
-            spans += (t.data_ptr(), t.numel(), dt)
-        struct.pack_into("@" + "PNi0P" * len(ts), self._array, 0, *spans)
-        self._ptrs = list(map(self._address, ts))
-        # element for element: an output needs its input's type and layout
-        self._layout = [(t.dtype, t.shape, t.stride()) for t in ts]
+        self._address = ctypes.addressof(self._array)
+        self.spans()
 
     def __len__(self):
         return len(self.tensors)
 
     def spans(self):
-        if list(map(self._address, self.tensors)) != self._ptrs:
-            self._fill()
+        """The tensors as a ctypes array of ar_span_t."""
+        self.index = (_bound and _bound[0] or binding()).spans(
+            self.tensors, self._address, len(self._array))  # their GPU; -1 without tensors
         return self._array
 
 
@@ -567,7 +445,7 @@ class Comm:
 
     def _stream(self, stream):
         if stream is None and self.workspace is not None:
-            raw = _raw_stream(self.workspace.get_device(), None)
+            raw = _raw_stream(self.workspace.get_device())
             if raw == self._ws_stream:
                 return raw
         import torch
@@ -617,26 +495,10 @@ class Comm:
         of residual, sum and y ([R, tokens * cols]) holds its own tokens;
         weight [cols] gives the row length; rstd is [R, tokens] and scale
         [R, tokens * ceil(cols / group)].  Otherwise as ``rmsnorm``."""
-        cols = weight.shape[0] if weight.dim() == 1 else 0
-        shape = y.shape
-        if len(shape) != 2 or shape[0] != self.R or (cols and shape[1] % cols):
-            raise ValueError("y must have shape (%d, tokens * %d), got %s"
-                             % (self.R, cols, tuple(shape)))
-        R, n = shape
-        tokens = n // cols if cols else 0
-        self._check_tensor(send, R, n * R, "send")
-        dtype, f32 = send.dtype, _f32()
-        dt, wdt, dev = _norm_types(send, weight, "send")
-        out, groups = _norm_output(send, y, scale, group, cols, dt)
-        rc = (_lib or lib()).ar_reduce_scatter_rmsnorm(
-            self.handle, send.data_ptr(), _pack_norm(
-                dt, out, wdt, eps, tokens, cols, group, 0, 0,
-                _block_of(residual, dev, shape, dtype, "residual"), 0,
-                _block_of(weight, dev, (cols,), weight.dtype, "weight"),
-                _block_of(sum, dev, shape, dtype, "sum"), 0,
-                _block_of(y, dev, shape, y.dtype, "y"), 0,
-                _block_of(scale, dev, (R, tokens * groups), f32, "scale"),
-                _block_of(rstd, dev, (R, tokens), f32, "rstd")), self._stream(stream))
+        self._check_tensor(send, self.R, send.shape[-1], "send")
+        rc = (_bound and _bound[0] or binding()).reduce_scatter_rmsnorm(
+            self.handle, send, weight, y, eps, residual, sum, scale, group, rstd,
+            self._stream(stream))
         if rc:
             raise ArError(rc, "ar_reduce_scatter_rmsnorm")
         return y
@@ -663,14 +525,15 @@ class Comm:
         if out is not None:
             out = _tensor_list(out)
             to = out.spans()
-            if out._layout != grads._layout or out.index != grads.index:
+            if out.index != grads.index or not binding().same_layout(grads.tensors, out.tensors):
                 raise ValueError("out must have the shapes, dtypes, strides and device of grads")
         ar_grad_clip(spans, to, len(grads), norm.data_ptr(), max_norm, self._stream(stream))
         return norm
 
     def _check_norm(self, grads, norm):
-        if norm.numel() != 1 or norm.dtype != _f32() or not norm.is_cuda or \
-                (grads.index is not None and grads.index != norm.get_device()):
+        import torch
+        if norm.numel() != 1 or norm.dtype != torch.float32 or not norm.is_cuda or \
+                (grads.index >= 0 and grads.index != norm.get_device()):
             raise ValueError("norm must be one float32 on the gradients' device")
 
     def check(self):

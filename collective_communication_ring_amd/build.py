@@ -1,4 +1,5 @@
-"""Build libar.so (HIP kernels for gfx950 + host communicator) in-tree.
+"""Build libar.so (HIP kernels for gfx950 + host communicator) in-tree, and the
+operators' Python marshalling (_binding.so).
 
 hipcc cross-compiles for gfx950 without a GPU.  Flags:
   -O3, no fast-math, -ffp-contract=off: every float add is one IEEE add;
@@ -6,10 +7,12 @@ hipcc cross-compiles for gfx950 without a GPU.  Flags:
   -Xclang -target-feature -Xclang -packed-fp32-ops: no packed fp32 ops
   (the host pass warns that it does not know the feature; harmless).
 """
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -17,6 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libar.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["ar_comm.cpp", "ar_ring.hip", "ar_fused.hip", "ar_pipe.hip", "ar_ring_ll.hip", "ar_tree.hip",
            "ar_tree_fused.hip", "ar_util.hip", "ar_noalloc.hip", "ar_ops.cpp", "ar_norm.hip",
            "ar_norm_back.hip", "ar_grad.hip"]
@@ -38,7 +42,7 @@ def _run(cmd, verbose, what):
                     if "packed-fp32-ops" not in l and "is not a recognized feature" not in l)
     if r.returncode != 0:
         sys.stderr.write(log + "\n")
-        raise RuntimeError("hipcc failed building %s" % what)
+        raise RuntimeError("%s failed building %s" % (os.path.basename(cmd[0]), what))
     if verbose and log.strip():
         print(log)
 
@@ -66,5 +70,21 @@ def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
     return out
 
 
+def build_binding(verbose: bool = False, out: str = BINDING) -> str:
+    """Compile the operators' argument marshalling (_binding.so, host code
+    against torch's own headers; it calls libar.so by addresses it is given)."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = out + ".tmp%d" % os.getpid()
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+          "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(torch_dir, "include"),
+          "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "py_binding.cpp"),
+          "-o", tmp, "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"],
+         verbose, "_binding.so")
+    os.replace(tmp, out)
+    return out
+
+
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_binding(verbose=True))
