@@ -302,7 +302,7 @@ void sort_reaches(std::vector<Reach>* v)
 bool clip_overlaps(const ar_span_t* in, const ar_span_t* out, size_t n, const float* norm)
 {
     std::vector<Reach> reads, writes;
-    reads.reserve(n + 1);
+    reads.reserve(n);
     writes.reserve(n);
     for (size_t i = 0; i < n; ++i) {
         const size_t bytes = in[i].count * size_of(in[i].dtype);
@@ -312,8 +312,9 @@ bool clip_overlaps(const ar_span_t* in, const ar_span_t* out, size_t n, const fl
         if (a != b)
             reads.push_back({a, a + bytes});
         writes.push_back({b, b + bytes});
+        if ((uintptr_t)norm < b + bytes && b < (uintptr_t)norm + sizeof(float))
+            return true;
     }
-    reads.push_back({(uintptr_t)norm, (uintptr_t)norm + sizeof(float)});
     sort_reaches(&reads);
     sort_reaches(&writes);
     for (size_t k = 1; k < writes.size(); ++k)

@@ -348,15 +348,15 @@ PyObject* spans(PyObject*, PyObject* const* a, Py_ssize_t n)
         int64_t device = -1;
         for (Py_ssize_t i = 0; i < count; ++i) {
             const at::Tensor& t = tensor(PyList_GET_ITEM(a[0], i), "a gradient");
-            const std::string which = "tensor " + std::to_string(i);
+            const auto which = [&] { return "tensor " + std::to_string(i); };
             const int dtype = code_of(t.scalar_type());
             if (dtype != AR_FLOAT32 && dtype != AR_BF16)
-                throw Refused(which + " has dtype " + type_text(t.scalar_type()) +
+                throw Refused(which() + " has dtype " + type_text(t.scalar_type()) +
                               ": float32 or bfloat16 is wanted");
             if (!t.is_cuda() || (i && t.get_device() != device))
-                throw Refused(which + " is on " + t.device().str() + ": all must be on one GPU");
+                throw Refused(which() + " is on " + t.device().str() + ": all must be on one GPU");
             if (!dense(t))
-                throw Refused(which + " is not dense in memory");
+                throw Refused(which() + " is not dense in memory");
             device = t.get_device();
             to[i] = {t.data_ptr(), (size_t)t.numel(), dtype};
         }
