@@ -137,8 +137,8 @@ __device__ inline void store_row(typename E::T* p, const float (&v)[NV][E::VEC],
 //
 // Bound by memory: bf16 8192 x 8192 with residual and e4m3 output moves its 472
 // MB in 75 us (6.3 TB/s; a copy of 1 GiB: 5.9).
-template <class E, bool WF32, bool Q, int NV, bool MULTI, int MAXT>
-__global__ __launch_bounds__(MAXT) void k_norm(NormArgs a)
+template <class E, bool WF32, bool Q, int NV, bool MULTI>
+__global__ __launch_bounds__(64 * kMaxWaves) void k_norm(NormArgs a)
 {
     using T = typename E::T;
     constexpr int V = E::VEC;
@@ -163,8 +163,9 @@ __global__ __launch_bounds__(MAXT) void k_norm(NormArgs a)
             res[k] = load_vec<E>(r, column(k), a.cols);
     }
     if constexpr (MULTI) {
-        // U ranks' vectors in flight at a time, added in the ring's order
-        constexpr int U = NV >= 4 ? (MAXT > 256 ? 1 : 2) : NV >= 2 ? 4 : 8;
+        // U ranks' vectors in flight at a time (as many as the registers of 1024
+        // threads hold), added in the ring's order
+        constexpr int U = NV >= 4 ? 1 : NV >= 2 ? 4 : 8;
         int p = (int)(t / a.tokens_per_rank);
         for (int i0 = 0; i0 < a.parts; i0 += U) {
             u32x4 raw[U][NV];
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(MAXT) void k_norm(NormArgs a)
                               h[k][4 * j + 3] * inv);
             if (c + V <= a.cols) {
                 // plain stores also where the others stream: 8 bytes a lane fill
-                // half a wave's lines (both streamed: 79 us of the 75)
+                // half a wave's lines (both streamed: 79 us instead of 75)
                 typedef uint32_t u32x2 __attribute__((ext_vector_type(2), aligned(1)));
                 typedef uint32_t u32 __attribute__((aligned(1)));
                 if constexpr (V == 8)
@@ -317,7 +318,7 @@ __global__ __launch_bounds__(MAXT) void k_norm(NormArgs a)
     }
 }
 
-template <class E, bool WF32, bool Q, int NV, bool MULTI, int MAXT>
+template <class E, bool WF32, bool Q, int NV, bool MULTI>
 void launch_row(NormArgs a, uint32_t nvec, hipStream_t s)
 {
     a.lanes = 64 * ((nvec + 64 * NV - 1) / (64 * NV));
@@ -329,7 +330,7 @@ void launch_row(NormArgs a, uint32_t nvec, hipStream_t s)
     const uint64_t most = kNormMaxThreads / a.lanes;  // a multiple of a workgroup's rows
     for (a.row0 = 0; a.row0 < a.rows; a.row0 += most) {
         const uint64_t n = std::min<uint64_t>(a.rows - a.row0, most);
-        hipLaunchKernelGGL((k_norm<E, WF32, Q, NV, MULTI, MAXT>), dim3((unsigned)((n + rows - 1) / rows)),
+        hipLaunchKernelGGL((k_norm<E, WF32, Q, NV, MULTI>), dim3((unsigned)((n + rows - 1) / rows)),
                            dim3(a.lanes * rows), 0, s, a);
     }
 }
@@ -343,11 +344,11 @@ void launch_typed(const NormArgs& a, hipStream_t s)
         hipLaunchKernelGGL((k_norm_any<E, Q>), dim3((unsigned)std::min<uint64_t>(a.rows, 1u << 16)),
                            dim3(kBlock), 0, s, a);
     else if (nvec > 64 * 2 * kMaxWaves)
-        launch_row<E, WF32, Q, 4, MULTI, 1024>(a, nvec, s);
+        launch_row<E, WF32, Q, 4, MULTI>(a, nvec, s);
     else if (nvec <= 64 || (nvec <= 64 * kMaxWaves && a.rows * nvec <= kFewVecs))
-        launch_row<E, WF32, Q, 1, MULTI, 1024>(a, nvec, s);
+        launch_row<E, WF32, Q, 1, MULTI>(a, nvec, s);
     else
-        launch_row<E, WF32, Q, 2, MULTI, 1024>(a, nvec, s);
+        launch_row<E, WF32, Q, 2, MULTI>(a, nvec, s);
 }
 
 template <class E, bool WF32, bool Q>

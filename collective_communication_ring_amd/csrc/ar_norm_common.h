@@ -173,11 +173,13 @@ __device__ inline uint32_t row_umax(uint32_t v, uint32_t* s, uint32_t w, uint32_
 }
 
 // r = 1 / sqrt(mean + eps).  A float32 sum of squares that is infinite may
-// have overflowed from finite elements: `again` then takes it in 64 bits.
+// have overflowed from finite elements, and one this small may have lost all
+// of them, where eps does not outweigh that: `again` then takes it in 64 bits.
 template <class Again>
 __device__ inline float inv_rms(float ss, uint32_t cols, float eps, Again again)
 {
-    if (ss == __builtin_inff())  // the same on every thread of the row
+    // the same on every thread of the row
+    if (ss == __builtin_inff() || (ss < 1e-25f && eps < 1e-20f))
         return (float)(1.0 / sqrt(again() / (double)cols + (double)eps));
     return 1.0f / sqrtf(ss / (float)cols + eps);
 }

@@ -403,7 +403,7 @@ int ar_ll_pingpong(void* lines, uint32_t* result_dev, int iters, int xcd_apart,
  * sum[t] receives h, y[t] receives v, rstd[t] receives r (sum and rstd may be
  * NULL).  h, r and v are float32, and h enters the norm as it is before sum's
  * rounding: every output is rounded once, to nearest even.  Sums of squares
- * are float32; where they pass its range they are taken again in 64 bits.
+ * are float32; where they leave its range they are taken again in 64 bits.
  * y in e4m3 (out_dtype AR_E4M3): a group is `group` consecutive columns (32,
  * 64, 128 or 256; 0: the whole row; the row's last group may be shorter), its
  * scale max(max |v| / 448, 2^-126) goes to scale[t][ceil(cols / group)], and y

@@ -104,6 +104,13 @@ def test_reduce_scatter_norm_refusals(api):
         api.ar_destroy(c)
 
 
+def test_e4m3_is_no_comm_type(api):
+    h = ctypes.c_void_p()
+    for algo in (api.AR_RING, api.AR_TREE, api.AR_AUTO):
+        assert api.lib().ar_init(ctypes.byref(h), 4, 64, api.AR_E4M3, algo, api.AR_SIMPLE) == \
+            api.AR_ERR_INVALID_ARG
+
+
 DY, BX, BW, BR, DS, DX, DW, WS = (0x20000000 * k for k in range(1, 9))
 
 

@@ -132,6 +132,26 @@ def test_norm_extreme_values(env, cols):
         _run_norm(env, 6, cols, dtype, out, 32 if out == "e4m3" else 0, dtype, False, x=x)
 
 
+@pytest.mark.parametrize("cols", (5, 100, 1000, 9000, 40000))
+@pytest.mark.parametrize("eps", (0.0, 1e-30))
+def test_norm_without_eps(env, cols, eps):
+    """No eps, or hardly any: rows whose squares float32 cannot hold, below
+    and above, and a row of zeros, 0 / 0 without eps."""
+    torch, api, dev = env["torch"], env["api"], env["dev"]
+    x = _rand(env, (5, cols), 14, torch.float32)
+    x[1] *= 2.0 ** -70   # squares about 2^-140
+    x[2] *= 2.0 ** -100  # squares are 0 in float32
+    x[3] *= 2.0 ** 80
+    _run_norm(env, 5, cols, "f32", "same", 0, "f32", False, x=x, eps=eps)
+    y, rstd = torch.ones((1, cols), device=dev), torch.zeros(1, device=dev)
+    api.rmsnorm(torch.zeros((1, cols), device=dev), torch.ones(cols, device=dev), y, eps, rstd=rstd)
+    torch.cuda.synchronize()
+    if eps:
+        assert (y == 0).all() and abs(float(rstd) * eps ** 0.5 - 1) < 4 * ob.U
+    else:
+        assert torch.isnan(y).all() and float(rstd) == math.inf
+
+
 @pytest.mark.parametrize("cols", (40, 1024, 8192, 40000))
 def test_norm_infinities_and_nan(env, cols):
     """An infinity makes its row's rstd 0: it becomes NaN (and its group's
