@@ -495,10 +495,9 @@ class Comm:
         of residual, sum and y ([R, tokens * cols]) holds its own tokens;
         weight [cols] gives the row length; rstd is [R, tokens] and scale
         [R, tokens * ceil(cols / group)].  Otherwise as ``rmsnorm``."""
-        self._check_tensor(send, self.R, send.shape[-1], "send")
         rc = (_bound and _bound[0] or binding()).reduce_scatter_rmsnorm(
             self.handle, send, weight, y, eps, residual, sum, scale, group, rstd,
-            self._stream(stream))
+            self._stream(stream), self.R, self.dtype, self.workspace.get_device())
         if rc:
             raise ArError(rc, "ar_reduce_scatter_rmsnorm")
         return y

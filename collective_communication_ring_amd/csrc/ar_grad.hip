@@ -171,9 +171,9 @@ __global__ __launch_bounds__(kBlock, 4) void k_grad_norm(SpanTable<kNormSpans> t
 }
 
 template <class E>
-__device__ inline void store_scaled(const Tile& tile, void* dst, float coef)
+__device__ inline void store_scaled(const Tile& tile, uint64_t dst, float coef)
 {
-    uint16_t* p = reinterpret_cast<uint16_t*>(static_cast<char*>(dst) + tile.offset);
+    uint16_t* p = reinterpret_cast<uint16_t*>(dst + tile.offset);
 #pragma unroll
     for (int k = 0; k < kTileNV; ++k) {
         float v[E::VEC];
@@ -186,15 +186,29 @@ __device__ inline void store_scaled(const Tile& tile, void* dst, float coef)
     }
 }
 
-__global__ __launch_bounds__(kBlock, 4) void k_grad_clip(SpanTable<kClipSpans> tab, SpanOutputs out,
-                                                         const float* norm, float max_norm)
+__device__ inline uint64_t output_of(const SpanOutputs& out, const Tile& tile)
+{
+    return out.dst[tile.span];
+}
+
+__device__ inline uint64_t output_of(const SpanShifts& out, const Tile& tile)
+{
+    const uint32_t i = (uint32_t)(tile.word >> 61) & 3u;
+    static_assert(kClipShifts == 4, "two bits of a span's word");
+    return (tile.word & kSpanAddress) +
+           (i == 0 ? out.by[0] : i == 1 ? out.by[1] : i == 2 ? out.by[2] : out.by[3]);
+}
+
+template <class Table, class Out>
+__global__ __launch_bounds__(kBlock, 4) void k_grad_clip(Table tab, Out out, const float* norm,
+                                                         float max_norm)
 {
     const float nv = *norm;
     const float c = max_norm / (nv + 1e-6f);
     const float coef = nv != nv ? nv : c < 1.0f ? c : 1.0f;
     for_tiles(tab, [&](const Tile& tile) {
-        void* dst = out.dst[tile.span];
-        if (coef == 1.0f && (uintptr_t)dst == (tile.word & kSpanAddress))
+        const uint64_t dst = output_of(out, tile);
+        if (coef == 1.0f && dst == (tile.word & kSpanAddress))
             return;  // in place, unchanged
         if (tile.word & kSpanBf16)
             store_scaled<Elem<AR_BF16>>(tile, dst, coef);
@@ -217,7 +231,16 @@ hipError_t launch_grad_norm(const SpanTable<kNormSpans>& t, void* scratch, int l
 hipError_t launch_grad_clip(const SpanTable<kClipSpans>& t, const SpanOutputs& o, const float* norm,
                             float max_norm, int grid, hipStream_t s)
 {
-    hipLaunchKernelGGL(k_grad_clip, dim3(grid), dim3(kBlock), 0, s, t, o, norm, max_norm);
+    hipLaunchKernelGGL((k_grad_clip<SpanTable<kClipSpans>, SpanOutputs>), dim3(grid), dim3(kBlock), 0,
+                       s, t, o, norm, max_norm);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const SpanTable<kNormSpans>& t, const SpanShifts& o, const float* norm,
+                            float max_norm, int grid, hipStream_t s)
+{
+    hipLaunchKernelGGL((k_grad_clip<SpanTable<kNormSpans>, SpanShifts>), dim3(grid), dim3(kBlock), 0, s,
+                       t, o, norm, max_norm);
     return hipGetLastError();
 }
 

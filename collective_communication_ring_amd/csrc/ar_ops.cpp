@@ -242,8 +242,8 @@ extern "C" int ar_rmsnorm_backward(const ar_rmsnorm_backward_t* args, void* stre
 
 namespace {
 
-// Largest tensor: the tiles of a whole table of such stay below 2^32 - 1.
-constexpr size_t kMaxSpan = (size_t)1 << 36;
+constexpr size_t kMaxSpan = (size_t)1 << 36;      // elements of a tensor: 256 GiB of float32
+constexpr uint64_t kMaxTiles = 0xfffffffeu;       // of a table (2^24 of the largest tensor)
 
 bool bad_span(const ar_span_t& s)
 {
@@ -252,9 +252,10 @@ bool bad_span(const ar_span_t& s)
 }
 
 // The next table of a list from span *i on, empty spans left out.
-template <class Table>
-void next_table(const ar_span_t* in, const ar_span_t* out, size_t n, size_t* i, Table* t,
-                SpanOutputs* o)
+// place(i, k, &shift): span i's output is that of entry k; false: not in this
+// table.
+template <class Table, class Place>
+void next_table(const ar_span_t* in, size_t n, size_t* i, Table* t, Place place)
 {
     t->tiles = 0;
     t->n = 0;
@@ -264,11 +265,12 @@ void next_table(const ar_span_t* in, const ar_span_t* out, size_t n, size_t* i, 
             continue;
         const uint64_t halves = s.count * size_of(s.dtype) / 2;
         const uint64_t tiles = (halves + kGradTileHalves - 1) / kGradTileHalves;
+        uint32_t shift = 0;
+        if (t->tiles + tiles > kMaxTiles || !place(*i, t->n, &shift))
+            break;
         t->span[t->n] = pack_span(s.data, (uint32_t)(halves - (tiles - 1) * kGradTileHalves),
-                                  s.dtype == AR_BF16);
+                                  s.dtype == AR_BF16, shift);
         t->first[t->n] = t->tiles;
-        if (o)
-            o->dst[t->n] = out[*i].data;
         t->tiles += (uint32_t)tiles;
         ++t->n;
     }
@@ -354,7 +356,7 @@ int grad_norm_run(const ar_span_t* grads, size_t n, float* norm, void* scratch, 
     size_t i = 0;
     do {  // a list of nothing has one table, of no spans: its norm is 0
         SpanTable<kNormSpans> t;
-        next_table(grads, nullptr, n, &i, &t, nullptr);
+        next_table(grads, n, &i, &t, [](size_t, int, uint32_t*) { return true; });
         const int grid = grid_for(t.tiles);
         *err = launch_grad_norm(t, scratch, live, grid, i == n ? norm : nullptr, s);
         if (*err != hipSuccess)
@@ -381,14 +383,37 @@ extern "C" int ar_grad_clip(const ar_span_t* grads, const ar_span_t* out, size_t
     } catch (...) {
         return AR_ERR_INTERNAL;
     }
+    hipStream_t st = static_cast<hipStream_t>(stream);
     for (size_t i = 0; i < n;) {
-        SpanTable<kClipSpans> t;
-        SpanOutputs o;
-        next_table(grads, out, n, &i, &t, &o);
-        if (!t.n)
-            break;
-        const hipError_t e = launch_grad_clip(t, o, norm, max_norm, grid_for(t.tiles),
-                                              static_cast<hipStream_t>(stream));
+        // by distances, if the table so made holds more than one of addresses would
+        size_t next = i;
+        SpanTable<kNormSpans> t;
+        SpanShifts by = {};
+        int shifts = 0;
+        next_table(grads, n, &next, &t, [&](size_t k, int, uint32_t* shift) {
+            const uint64_t d = (uint64_t)(uintptr_t)out[k].data - (uint64_t)(uintptr_t)grads[k].data;
+            while (*shift < (uint32_t)shifts && by.by[*shift] != d)
+                ++*shift;
+            if (*shift == kClipShifts)
+                return false;
+            if (*shift == (uint32_t)shifts)
+                by.by[shifts++] = d;
+            return true;
+        });
+        hipError_t e = hipSuccess;
+        if (next == n || t.n >= kClipSpans) {
+            if (t.n)
+                e = launch_grad_clip(t, by, norm, max_norm, grid_for(t.tiles), st);
+            i = next;
+        } else {
+            SpanTable<kClipSpans> u;
+            SpanOutputs o;
+            next_table(grads, n, &i, &u, [&](size_t k, int at, uint32_t*) {
+                o.dst[at] = (uint64_t)(uintptr_t)out[k].data;
+                return true;
+            });
+            e = launch_grad_clip(u, o, norm, max_norm, grid_for(u.tiles), st);
+        }
         if (e != hipSuccess)
             return done(e);
     }

@@ -100,15 +100,20 @@ constexpr uint32_t kGradTileHalves = kGradTileVecs * 8;  // in 16-bit units, as 
 // A table of spans is passed by value in a launch's kernel arguments: no copy
 // to the device, and a captured graph keeps its own.  A span is packed into one
 // word -- its address (48 bits), the 16-bit units of its last tile less one (13
-// bits), and whether it is bfloat16 -- so that 4 KiB of arguments hold
-// kNormSpans of them, or kClipSpans with an output address each.
+// bits), which of kClipShifts distances its output lies at (2 bits), and
+// whether it is bfloat16 -- so that 4 KiB of arguments hold kNormSpans of them,
+// or kClipSpans with an output address each.  Outputs in place or cut from a
+// few buffers as their inputs are need the distances alone: 291 tensors are
+// clipped by one launch instead of two.
 constexpr int kNormSpans = 312;
 constexpr int kClipSpans = 184;
+constexpr int kClipShifts = 4;
 constexpr uint64_t kSpanAddress = ((uint64_t)1 << 48) - 1;
 constexpr uint64_t kSpanBf16 = (uint64_t)1 << 63;
-inline uint64_t pack_span(const void* p, uint32_t last_halves, bool bf16)
+inline uint64_t pack_span(const void* p, uint32_t last_halves, bool bf16, uint32_t shift)
 {
-    return (uint64_t)(uintptr_t)p | (uint64_t)(last_halves - 1) << 48 | (bf16 ? kSpanBf16 : 0);
+    return (uint64_t)(uintptr_t)p | (uint64_t)(last_halves - 1) << 48 | (uint64_t)shift << 61 |
+           (bf16 ? kSpanBf16 : 0);
 }
 
 template <int N>
@@ -121,8 +126,13 @@ struct SpanTable {
     int n;
 };
 
+// Where a table's outputs are: an address each, or the distances (modulo 2^64)
+// from input to output.
 struct SpanOutputs {
-    void* dst[kClipSpans];
+    uint64_t dst[kClipSpans];
+};
+struct SpanShifts {
+    uint64_t by[kClipShifts];
 };
 
 // Workgroups of a launch, at most: 2 on each of 256 CUs.  They take the tiles
@@ -148,6 +158,8 @@ constexpr size_t kGradScratchBytes =
 hipError_t launch_grad_norm(const SpanTable<kNormSpans>& t, void* scratch, int live, int grid, float* norm,
                             hipStream_t s);
 hipError_t launch_grad_clip(const SpanTable<kClipSpans>& t, const SpanOutputs& o, const float* norm,
+                            float max_norm, int grid, hipStream_t s);
+hipError_t launch_grad_clip(const SpanTable<kNormSpans>& t, const SpanShifts& o, const float* norm,
                             float max_norm, int grid, hipStream_t s);
 
 // Tables of a list, one after the other (ar_ops.cpp).  ar_grad_norm's work.

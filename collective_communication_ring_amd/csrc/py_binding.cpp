@@ -247,26 +247,29 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
-// reduce_scatter_rmsnorm(comm, send, weight, y, eps, residual, sum, scale, group, rstd, stream)
-// -> status; send has been checked against the comm
+// reduce_scatter_rmsnorm(comm, send, weight, y, eps, residual, sum, scale, group, rstd, stream,
+// ranks, dtype, device) -> status; the last three are the comm's
 PyObject* reduce_scatter_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
-        expect(n, 11);
+        expect(n, 14);
         const at::Tensor &send = tensor(a[1], "send"), &weight = tensor(a[2], "weight"),
                          &y = tensor(a[3], "y");
         const at::Tensor *residual = tensor_or_none(a[5], "residual"),
                          *sum = tensor_or_none(a[6], "sum"), *scale = tensor_or_none(a[7], "scale"),
                          *rstd = tensor_or_none(a[9], "rstd");
         const int64_t cols = weight.dim() == 1 ? weight.size(0) : 0, group = integer(a[8]);
-        if (send.dim() != 2 || y.dim() != 2 || y.size(0) != send.size(0) ||
-            (cols && y.size(1) % cols) || y.size(1) * y.size(0) != send.size(1))
-            throw Refused("y must have shape (ranks, tokens * " + std::to_string(cols) +
-                          ") and send (ranks, ranks * tokens * cols), got " + shape_text(y.sizes()) +
-                          " and " + shape_text(send.sizes()));
-        const int64_t R = y.size(0), tokens = cols ? y.size(1) / cols : 0;
+        const int64_t R = integer(a[11]);
+        if (y.dim() != 2 || y.size(0) != R || (cols ? y.size(1) % cols : y.size(1)))
+            throw Refused("y must have shape (" + std::to_string(R) + ", tokens * " +
+                          std::to_string(cols) + "), got " + shape_text(y.sizes()));
+        const int64_t tokens = cols ? y.size(1) / cols : 0;
         ar_rmsnorm_t p = {};
         norm_types(send, weight, "send", &p.dtype, &p.weight_dtype);
+        if (p.dtype != integer(a[12]))
+            throw Refused("send has dtype " + type_text(send.scalar_type()) + ", the comm another");
+        const int64_t all[] = {R, R * y.size(1)};
+        const void* from = block_of(send, integer(a[13]), all, send.scalar_type(), "send");
         const int64_t groups = norm_output(send, y, scale, group, cols, p.dtype, &p.out_dtype);
         const int64_t dev = send.get_device();
         const at::ScalarType type = send.scalar_type();
@@ -286,7 +289,7 @@ PyObject* reduce_scatter_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (rstd)
             p.rstd = static_cast<float*>(block_of(*rstd, dev, per, at::kFloat, "rstd"));
         return PyLong_FromLong(p_reduce_scatter_rmsnorm(static_cast<ar_comm_t>(handle(a[0])),
-                                                        send.data_ptr(), &p, handle(a[10])));
+                                                        from, &p, handle(a[10])));
     });
 }
 

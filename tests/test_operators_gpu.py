@@ -459,6 +459,39 @@ def test_clip_many_tensors(env, count):
     _check_clip(env, _many(env, sizes, offsets=True), 0.1, False)
 
 
+@pytest.mark.parametrize("count", (3, 190, 400))
+@pytest.mark.parametrize("buffers", (1, 4, 5, 97))
+def test_clip_into_buffers(env, count, buffers):
+    """Outputs cut from a number of buffers in turn: at up to four distances
+    from their inputs a table holds no addresses of outputs."""
+    torch, dev = env["torch"], env["dev"]
+    sizes = [(i * 911) % 3001 + 1 for i in range(count)]
+    total = sum(sizes) + 8
+    src = _rand(env, (total,), 3, torch.float32, 0.02).bfloat16().to(dev)
+    dst = [torch.full((total,), 7.0, device=dev).bfloat16() for _ in range(buffers)]
+    comm = env["api"].Comm(2, 4, "float32", device=dev)
+    norm = torch.full((1,), 3.0, device=dev)
+    grads, out, lo = [], [], 3
+    for i, n in enumerate(sizes):
+        grads.append(src[lo:lo + n])
+        out.append(dst[i % buffers][lo:lo + n])
+        lo += n
+    comm.grad_clip(grads, norm, 0.75, out=out)
+    torch.cuda.synchronize()
+    c = 0.75 / (3.0 + 1e-6)
+    for g, o in zip(grads, out):
+        v = g.cpu().double() * c
+        ob.between(o, v, 3.001 * ob.U * v.abs(), "clipped")
+    for k, d in enumerate(dst):  # and nothing beside them
+        want, lo = torch.full_like(d, 7.0), 3
+        for i, n in enumerate(sizes):
+            if i % buffers == k:
+                want[lo:lo + n] = out[i]
+            lo += n
+        assert torch.equal(d, want)
+    comm.close()
+
+
 def test_clip_tensor_list(env):
     """A TensorList kept over calls, dense tensors of any dimension order, and
     an address that changes under it."""
