@@ -149,10 +149,13 @@ __global__ __launch_bounds__(kBlock, 4) void k_grad_norm(SpanTable<kNormSpans> t
             const uint32_t group = blockIdx.x / kTicketGroup;
             const uint32_t groups = (gridDim.x + kTicketGroup - 1) / kTicketGroup;
             const uint32_t left = gridDim.x - group * kTicketGroup;
-            uint32_t* mine = tickets + (group + 1) * kTicketLine;
+            uint32_t* mine = tickets + group * kTicketLine;
+            uint32_t* top = tickets + kTicketTop * kTicketLine;
             if (last_ticket(mine, left < kTicketGroup ? left : kTicketGroup)) {
                 __hip_atomic_store(mine, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                s_last = last_ticket(tickets, groups);
+                s_last = groups == 1 || last_ticket(top, groups);
+                if (s_last && groups > 1)
+                    __hip_atomic_store(top, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
         }
     }
@@ -164,10 +167,8 @@ __global__ __launch_bounds__(kBlock, 4) void k_grad_norm(SpanTable<kNormSpans> t
     for (int i = threadIdx.x; i < n; i += kBlock)
         sum += __hip_atomic_load(slots + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     sum = block_sum<W>(sum, s_d);
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0)
         *norm = (float)sqrt(sum);
-        __hip_atomic_store(tickets, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
 }
 
 template <class E>

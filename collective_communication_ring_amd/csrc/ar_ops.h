@@ -148,8 +148,9 @@ constexpr int kGradMaxBlocks = 512;
 // norm by 2048 workgroups: 34 us, 16 us with the groups).
 constexpr int kTicketGroup = 32;
 constexpr int kTicketLine = 32;  // uint32 words
+constexpr int kTicketTop = kGradMaxBlocks / kTicketGroup;  // the groups' own counter
 constexpr size_t kGradScratchBytes =
-    (size_t)kGradMaxBlocks * 8 + (size_t)(kGradMaxBlocks / kTicketGroup + 1) * kTicketLine * 4;
+    (size_t)kGradMaxBlocks * 8 + (size_t)(kTicketTop + 1) * kTicketLine * 4;
 
 // Sums of squares of one table's spans.  Slots [0, live) of `scratch` hold the
 // sums of the tables before it, to which this one adds.  `norm` (the last
