@@ -200,6 +200,54 @@ def test_norm_in_place(env, dtype, cols):
         assert torch.equal(out, y) and torch.equal(s, h), how
 
 
+def _guarded(env, rows, cols, dtype, pad, offset):
+    """Rows of a wider array whose other elements hold a mark, the array, and a
+    check that these still do."""
+    torch = env["torch"]
+    flat = torch.full((offset + rows * (cols + pad) + 40,), 3.0, device=env["dev"]).to(dtype)
+    view = flat[offset:offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+
+    def untouched():
+        rest = flat.clone()
+        rest[offset:offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols] = 3.0
+        assert (rest.float() == 3.0).all()
+    return view, untouched
+
+
+@pytest.mark.parametrize("cols,pad,offset", [
+    (1, 3, 1), (5, 2, 0), (8, 1, 3), (63, 1, 2), (64, 8, 8), (500, 7, 1), (1001, 3, 5), (2057, 1, 1),
+    (4099, 5, 0), (8192, 16, 0), (9001, 2, 1), (17003, 1, 1), (33001, 3, 1),
+])
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+def test_nothing_beside_the_outputs_is_written(env, dtype, cols, pad, offset):
+    torch, api, dev = env["torch"], env["api"], env["dev"]
+    dt = _types(torch)[dtype]
+    rows, e4m3, f32 = 5, torch.float8_e4m3fn, torch.float32
+    x, res, dy = (_rand(env, (rows, cols), s, dt).to(dev) for s in (1, 2, 3))
+    w = torch.ones(cols, device=dev, dtype=dt)
+    for group in (None, 0, 32):
+        groups = -(-cols // group) if group else 1
+        outs = {"y": _guarded(env, rows, cols, dt if group is None else e4m3, pad, offset),
+                "sum": _guarded(env, rows, cols, dt, pad, 2 * offset),
+                "rstd": _guarded(env, 1, rows, f32, pad, offset)}
+        if group is not None:
+            outs["scale"] = _guarded(env, 1, rows * groups, f32, pad, offset)
+        o = {k: v[0] for k, v in outs.items()}
+        api.rmsnorm(x, w, o["y"], EPS, residual=res, sum=o["sum"], rstd=o["rstd"][0], group=group or 0,
+                    scale=o["scale"].view(rows, groups) if group is not None else None)
+        torch.cuda.synchronize()
+        for _, untouched in outs.values():
+            untouched()
+    r = torch.ones(rows, device=dev)
+    dx, untouched_dx = _guarded(env, rows, cols, dt, pad, offset)
+    dw, untouched_dw = _guarded(env, 1, cols, f32, pad, offset)
+    ws, untouched_ws = _guarded(env, 1, max(64, api.ar_rmsnorm_backward_workspace(1, rows, cols) // 4),
+                                f32, 0, 64)
+    api.rmsnorm_backward(dy, x, w, r, dx, dw, dsum=res, workspace=ws[0])
+    torch.cuda.synchronize()
+    untouched_dx(), untouched_dw(), untouched_ws()
+
+
 def test_norm_interleaved_rows(env):
     """x and y as the halves of one array's rows: no overlap."""
     torch, api, dev = env["torch"], env["api"], env["dev"]
