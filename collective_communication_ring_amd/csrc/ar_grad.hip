@@ -15,6 +15,7 @@ constexpr int kTileNV = kGradTileVecs / kBlock;  // a thread's vectors of a tile
 
 struct Tile {
     uint32_t span;
+    uint32_t first, end;  // the span's tiles
     uint64_t word;     // the span's
     uint64_t offset;   // bytes from the span's start
     uint32_t halves;   // 16-bit units
@@ -34,9 +35,15 @@ __device__ inline void find_tile(const Table& tab, uint32_t t, Tile* o)
     const uint32_t s = (uint32_t)__builtin_amdgcn_readfirstlane(n) - 1;
     o->span = s;
     o->word = tab.span[s];
-    const uint32_t end = s + 1 < (uint32_t)tab.n ? tab.first[s + 1] : tab.tiles;
-    o->offset = (uint64_t)(t - tab.first[s]) * (kGradTileVecs * 16u);
-    o->halves = t + 1 == end ? ((uint32_t)(o->word >> 48) & 0x1fffu) + 1 : kGradTileHalves;
+    o->first = tab.first[s];
+    o->end = s + 1 < (uint32_t)tab.n ? tab.first[s + 1] : tab.tiles;
+}
+
+// Where tile t of its span lies.
+__device__ inline void place_tile(uint32_t t, Tile* o)
+{
+    o->offset = (uint64_t)(t - o->first) * (kGradTileVecs * 16u);
+    o->halves = t + 1 == o->end ? ((uint32_t)(o->word >> 48) & 0x1fffu) + 1 : kGradTileHalves;
 }
 
 // All loads of a tile in flight together, the same for both types.  Non-
@@ -86,13 +93,20 @@ __device__ inline void for_tiles(const Table& tab, Work work)
         return;
     Tile cur;
     find_tile(tab, t, &cur);
+    place_tile(t, &cur);
     load_tile(&cur);
     for (;;) {
         t += gridDim.x;
         if (t >= tab.tiles || t < gridDim.x)
             break;
         Tile next;
-        find_tile(tab, t, &next);
+        next.span = cur.span;
+        next.word = cur.word;
+        next.first = cur.first;
+        next.end = cur.end;
+        if (t >= cur.end)
+            find_tile(tab, t, &next);
+        place_tile(t, &next);
         load_tile(&next);
         fit_tile(&cur);
         work(cur);

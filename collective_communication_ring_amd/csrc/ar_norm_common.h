@@ -65,7 +65,30 @@ __device__ inline float wave_sum(float v)
     return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 
-__device__ inline double wave_sum(double v) { return lanes_sum(v, 64u); }
+template <int CTRL>
+__device__ inline double dpp(double v)
+{
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    return __longlong_as_double((long long)((uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 |
+                                            dpp<CTRL>((uint32_t)u)));
+}
+
+__device__ inline double lane_of(double v, int lane)
+{
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+__device__ inline double wave_sum(double v)
+{
+    v += dpp<kXor1>(v);
+    v += dpp<kXor2>(v);
+    v += dpp<kMirror8>(v);
+    v += dpp<kMirror16>(v);
+    return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+}
 
 __device__ inline uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
