@@ -139,8 +139,8 @@ struct SpanShifts {
 // Workgroups of a launch, at most: 2 on each of 256 CUs.  They take the tiles
 // in turn (tile t goes to workgroup t mod grid), so that the whole grid reads
 // one stretch of memory at a time: 40 x 25 MiB of bfloat16 normed and clipped
-// in 510 us (6.3 TB/s over its three passes), against 569 us with a stretch of
-// its own for each workgroup.  1024 workgroups: the same 510 us, and 15.1 us
+// in 504 us (6.2 TB/s over its three passes), against 569 us with a stretch of
+// its own for each workgroup.  1024 workgroups: the same there, and 15.1 us
 // for a norm of 64 MiB against 14.3.
 constexpr int kGradMaxBlocks = 512;
 // Workgroups take tickets in groups of this many, each group's counter in a
