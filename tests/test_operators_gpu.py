@@ -200,6 +200,30 @@ def test_norm_in_place(env, dtype, cols):
         assert torch.equal(out, y) and torch.equal(s, h), how
 
 
+@pytest.mark.parametrize("cols", (70, 4096, 40000))
+def test_e4m3_of_a_product_that_overflows(env, cols):
+    """v = h r w past float32's range: its group's scale is infinite, it
+    becomes NaN and the rest of the group 0; the other groups are as without."""
+    torch, api, dev = env["torch"], env["api"], env["dev"]
+    x = _rand(env, (3, cols), 2, torch.float32)
+    x[:, 40] = 3.0
+    w = torch.ones(cols)
+    w[40] = 3e38
+    groups = -(-cols // 32)
+    q = torch.empty((3, cols), device=dev, dtype=torch.float8_e4m3fn)
+    scale = torch.empty((3, groups), device=dev)
+    api.rmsnorm(x.to(dev), w.to(dev), q, EPS, scale=scale, group=32)
+    torch.cuda.synchronize()
+    w[40] = 1.0  # for the other groups
+    form = ob.norm(x, w, EPS, group=32)
+    keep = torch.ones(cols, dtype=torch.bool)
+    keep[32:64] = False
+    ob.between(q[:, keep.to(dev)], *(t[:, keep] for t in form["y"]), "y")
+    q, scale = q.cpu().float(), scale.cpu()
+    assert (scale[:, 1] == math.inf).all() and torch.isnan(q[:, 40]).all()
+    assert (q[:, 32:40] == 0).all() and (q[:, 41:64] == 0).all()
+
+
 def _guarded(env, rows, cols, dtype, pad, offset):
     """Rows of a wider array whose other elements hold a mark, the array, and a
     check that these still do."""
