@@ -86,12 +86,11 @@ __global__ __launch_bounds__(kBlock) void k_norm_any(NormArgs a)
                 }
                 m = whole ? block_umax<W>(m, s_u) : wave_umax(m);
                 const float scale = e4m3_scale(m);
-                const float inv = 1.0f / scale;
                 if (lane == 0)
                     a.scale[t * a.groups + g] = scale;
                 for (uint32_t c = lo + lane; c < hi; c += step) {
                     const float h = value(c);
-                    y[t * a.y_stride + c] = e4m3(normed(c, h) * inv);
+                    y[t * a.y_stride + c] = e4m3(normed(c, h) / scale);
                     if (sum)
                         sum[t * a.sum_stride + c] = E::narrow(h);
                 }
@@ -293,14 +292,14 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_norm(NormArgs a)
         for (int k = 0; k < NV; ++k) {
             const uint32_t c = column(k);
             const float scale = e4m3_scale(m[k]);
-            const float inv = 1.0f / scale;
             if (c < a.cols && c % a.group == 0)
                 a.scale[t * a.groups + c / a.group] = scale;
+            float quot[V];
+            over_scale<V>(h[k], scale, quot);
             u32x4 q = {0u, 0u, 0u, 0u};
 #pragma unroll
             for (int j = 0; j < V / 4; ++j)
-                q[j] = e4m3x4(h[k][4 * j] * inv, h[k][4 * j + 1] * inv, h[k][4 * j + 2] * inv,
-                              h[k][4 * j + 3] * inv);
+                q[j] = e4m3x4(quot[4 * j], quot[4 * j + 1], quot[4 * j + 2], quot[4 * j + 3]);
             if (c + V <= a.cols) {
                 // plain stores also where the others stream: 8 bytes a lane fill
                 // half a wave's lines (both streamed: 79 us instead of 75)

@@ -407,8 +407,9 @@ int ar_ll_pingpong(void* lines, uint32_t* result_dev, int iters, int xcd_apart,
  * y in e4m3 (out_dtype AR_E4M3): a group is `group` consecutive columns (32,
  * 64, 128 or 256; 0: the whole row; the row's last group may be shorter), its
  * scale max(max |v| / 448, 2^-126) goes to scale[t][ceil(cols / group)], and y
- * holds v / scale in e4m3.  A group with an infinity has an infinite
- * scale, its infinities become NaN and the rest 0; one with a NaN is all NaN.
+ * holds v / scale, a float32 quotient, in e4m3.  A group with an infinity has
+ * an infinite scale, its infinities become NaN and the rest 0; one with a NaN
+ * is all NaN.
  * x, residual, sum and y rows are `*_stride` apart (>= cols; ignored when
  * rows is 1), columns are contiguous; scale and rstd are contiguous.  An
  * output may share x's or residual's array, with the same address, stride and
