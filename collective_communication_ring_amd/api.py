@@ -378,10 +378,15 @@ def rmsnorm_backward(dy, x, weight, rstd, dx, dweight, dsum=None, workspace=None
     ``ranks`` equal shards of the rows.  dx may be dy, x or dsum.  Without
     ``workspace`` (``rmsnorm_backward_workspace``) one is allocated."""
     if workspace is None:
-        workspace = rmsnorm_backward_workspace(
-            dweight.shape[0], x.shape[0], x.shape[-1], x.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        size = dweight.shape[0], x.shape[0], x.shape[-1], x.device
+        if stream is None:
+            workspace = rmsnorm_backward_workspace(*size)
+        else:
+            # from that stream's memory: what was freed on the current one may
+            # still be in use there
+            import torch
+            with torch.cuda.stream(stream):
+                workspace = rmsnorm_backward_workspace(*size)
     rc = (_bound and _bound[0] or binding()).rmsnorm_backward(
         dy, x, weight, rstd, dx, dweight, dsum, workspace, _stream_of(x, stream))
     if rc:
