@@ -56,16 +56,17 @@ bool same(const Rows& a, const Rows& b)
     return a.at == b.at && a.len == b.len && (a.rows == 1 || a.stride == b.stride);
 }
 
-// Outputs against each other and against the inputs.  in[0 .. in_place) may be
-// an output's array.
-bool disjoint(const Rows* out, int nout, const Rows* in, int nin, int in_place)
+// Outputs against each other and against the inputs.  out[0 .. replacing) may
+// have the array of one of in[0 .. replaced); the others are of another kind,
+// whatever their address and length.
+bool disjoint(const Rows* out, int nout, int replacing, const Rows* in, int nin, int replaced)
 {
     for (int i = 0; i < nout; ++i) {
         for (int j = i + 1; j < nout; ++j)
             if (share(out[i], out[j]))
                 return false;
         for (int j = 0; j < nin; ++j)
-            if (share(out[i], in[j]) && !(j < in_place && same(out[i], in[j])))
+            if (share(out[i], in[j]) && !(i < replacing && j < replaced && same(out[i], in[j])))
                 return false;
     }
     return true;
@@ -150,7 +151,7 @@ int norm_prepare(ar_rmsnorm_t p, int parts, NormArgs* out, bool* noop)
                          rows_of(a.scale, 1, p.rows * a.groups, 0, AR_FLOAT32),
                          rows_of(p.rstd, 1, p.rows, 0, AR_FLOAT32)};
     const Rows ins[] = {res, x, w};
-    if (!disjoint(outs, 4, ins, 3, parts > 1 ? 1 : 2))
+    if (!disjoint(outs, 4, 2, ins, 3, parts > 1 ? 1 : 2))
         return AR_ERR_INVALID_USAGE;
     *out = a;
     return AR_SUCCESS;
@@ -214,7 +215,7 @@ extern "C" int ar_rmsnorm_backward(const ar_rmsnorm_backward_t* args, void* stre
                             rows_of(p.dsum, p.rows, p.cols, p.dsum_stride, p.dtype),
                             rows_of(p.weight, 1, p.cols, 0, p.weight_dtype),
                             rows_of(p.rstd, 1, p.rows, 0, AR_FLOAT32)};
-        if (!disjoint(outs, 3, ins, 5, 3))
+        if (!disjoint(outs, 3, 1, ins, 5, 3))
             return AR_ERR_INVALID_USAGE;
     }
     NormBackArgs a{};

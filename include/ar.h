@@ -411,10 +411,10 @@ int ar_ll_pingpong(void* lines, uint32_t* result_dev, int iters, int xcd_apart,
  * an infinite scale, its infinities become NaN and the rest 0; one with a NaN
  * is all NaN.
  * x, residual, sum and y rows are `*_stride` apart (>= cols; ignored when
- * rows is 1), columns are contiguous; scale and rstd are contiguous.  An
- * output may share x's or residual's array, with the same address, stride and
- * type; any other overlap of an output is AR_ERR_INVALID_USAGE (rows
- * interleaved in one array with one stride do not overlap).
+ * rows is 1), columns are contiguous; scale and rstd are contiguous.  sum or y
+ * may have x's or residual's array, with the same address, stride and type;
+ * any other overlap of an output is AR_ERR_INVALID_USAGE (rows interleaved in
+ * one array with one stride do not overlap).
  * rows == 0 or cols == 0 is a successful no-op.  cols is at most 2^28. */
 typedef struct {
     int dtype;        /* AR_FLOAT32 or AR_BF16: x, residual, sum */
