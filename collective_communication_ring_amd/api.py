@@ -500,6 +500,8 @@ class Comm:
         of residual, sum and y ([R, tokens * cols]) holds its own tokens;
         weight [cols] gives the row length; rstd is [R, tokens] and scale
         [R, tokens * ceil(cols / group)].  Otherwise as ``rmsnorm``."""
+        if self.workspace is None:  # closed
+            raise ArError(AR_ERR_INVALID_ARG, "ar_reduce_scatter_rmsnorm")
         rc = (_bound and _bound[0] or binding()).reduce_scatter_rmsnorm(
             self.handle, send, weight, y, eps, residual, sum, scale, group, rstd,
             self._stream(stream), self.R, self.dtype, self.workspace.get_device())
