@@ -541,6 +541,10 @@ class Comm:
         if norm.numel() != 1 or norm.dtype != torch.float32 or not norm.is_cuda or \
                 (grads.index >= 0 and grads.index != norm.get_device()):
             raise ValueError("norm must be one float32 on the gradients' device")
+        # the stream and the partial sums are those of the communicator's GPU
+        if self.workspace is not None and norm.get_device() != self.workspace.get_device():
+            raise ValueError("norm is on cuda:%d, the comm on cuda:%d" %
+                             (norm.get_device(), self.workspace.get_device()))
 
     def check(self):
         return ar_check(self.handle)
