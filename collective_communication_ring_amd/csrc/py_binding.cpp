@@ -188,6 +188,18 @@ PyObject* guarded(Call call)
     return nullptr;
 }
 
+// An entry point's status.  Other Python threads run meanwhile: a launch may
+// have to wait for room in its stream's queue.
+template <class F, class... Args>
+PyObject* status_of(F entry, Args... args)
+{
+    int rc = 0;
+    Py_BEGIN_ALLOW_THREADS
+    rc = entry(args...);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
 void expect(Py_ssize_t got, Py_ssize_t want)
 {
     if (got != want)
@@ -243,7 +255,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n)
             p.scale = static_cast<float*>(block_of(*scale, dev, scales, at::kFloat, "scale"));
         if (rstd)
             p.rstd = static_cast<float*>(block_of(*rstd, dev, {rows}, at::kFloat, "rstd"));
-        return PyLong_FromLong(p_rmsnorm(&p, handle(a[9])));
+        return status_of(p_rmsnorm, &p, handle(a[9]));
     });
 }
 
@@ -288,8 +300,8 @@ PyObject* reduce_scatter_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n)
             p.scale = static_cast<float*>(block_of(*scale, dev, scales, at::kFloat, "scale"));
         if (rstd)
             p.rstd = static_cast<float*>(block_of(*rstd, dev, per, at::kFloat, "rstd"));
-        return PyLong_FromLong(p_reduce_scatter_rmsnorm(static_cast<ar_comm_t>(handle(a[0])),
-                                                        from, &p, handle(a[10])));
+        return status_of(p_reduce_scatter_rmsnorm, static_cast<ar_comm_t>(handle(a[0])), from, &p,
+                         handle(a[10]));
     });
 }
 
@@ -329,7 +341,7 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
         p.dweight = static_cast<float*>(block_of(dweight, dev, wshape, at::kFloat, "dweight"));
         p.workspace = workspace.data_ptr();
         p.workspace_bytes = (size_t)workspace.nbytes();
-        return PyLong_FromLong(p_rmsnorm_backward(&p, handle(a[8])));
+        return status_of(p_rmsnorm_backward, &p, handle(a[8]));
     });
 }
 
