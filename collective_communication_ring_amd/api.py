@@ -512,8 +512,8 @@ class Comm:
     def grad_norm(self, grads, norm, stream=None):
         """Global 2-norm of the tensors of ``grads`` (a sequence, or a
         ``TensorList`` kept for many calls) to ``norm``, one float32 on the
-        device (``ar_grad_norm``).  Uses the comm's workspace: ordered with its
-        collectives on one stream."""
+        device (``ar_grad_norm``), all on the comm's GPU.  Uses the comm's
+        workspace: ordered with its collectives on one stream."""
         grads = _tensor_list(grads)
         spans = grads.spans()
         self._check_norm(grads, norm)

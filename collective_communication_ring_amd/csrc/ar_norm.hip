@@ -23,6 +23,10 @@ constexpr uint64_t kFewVecs = 256 * 16 * 64;
 // Each pass reads the row again (from L2, except the first).  A thread reads
 // an element before it writes that element's outputs, and no other thread
 // touches it, so an output may be an input's array.
+//
+// For rows of less than a vector, and the longest: two- and four-byte accesses
+// keep it from memory's rate (float32 4096 x 18,432 with residual: 412 us for
+// 1.2 GB, 2.9 TB/s; bf16 2048 x 40,000: 676 us for 0.66 GB).
 template <class E, bool Q>
 __global__ __launch_bounds__(kBlock) void k_norm_any(NormArgs a)
 {
@@ -135,8 +139,8 @@ __device__ inline void store_row(typename E::T* p, const float (&v)[NV][E::VEC],
 // other thread uses them, so an output may be an input's array.
 //
 // Bound by memory: bf16 8192 x 8192 with residual and e4m3 output moves its 472
-// MB in 74 us (6.4 TB/s; a copy of 1 GiB: 5.9), 8 ranks' 2048 x 8192 reduced and
-// normed to e4m3 their 353 MB in 60 us (5.8 TB/s).
+// MB in 75 us (6.3 TB/s; a copy of 1 GiB: 5.9), 8 ranks' 2048 x 8192 reduced and
+// normed to e4m3 their 353 MB in 61 us (5.8 TB/s).
 template <class E, bool WF32, bool Q, int NV, bool MULTI>
 __global__ __launch_bounds__(64 * kMaxWaves) void k_norm(NormArgs a)
 {

@@ -275,6 +275,10 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_back(NormBackArgs a)
 // flight.  Else it is read twice, the second time out of the caches; all of its
 // first reads come before its writes, and the second ones are of what the same
 // thread writes.
+//
+// float32 4096 x 8192 with dsum 116 us (4.6 TB/s), bf16 2048 x 16,384 69 us (3.9
+// TB/s), 2048 x 32,768 159 us (3.4 TB/s): besides the rows, the weight's reads
+// and the sums' in LDS for every row, and the partial rows.
 template <class E, bool WF32, int NV, bool HOLD>
 __global__ __launch_bounds__(64 * kMaxWaves) void k_back_long(NormBackArgs a)
 {

@@ -80,8 +80,8 @@ constexpr uint64_t kNormMaxThreads = (uint64_t)1 << 31;
 // and rows that do not fill their last lines lose by it (2568: 33 -> 35 us).
 constexpr uint64_t kStreamBytes = (uint64_t)32 << 20;
 // Partial rows of dweight of all ranks, at most: a workgroup of 16 waves on each
-// CU, all resident (bf16 8192 x 8192: 93 us; 512 workgroups of 8 waves 96, 768
-// of 5 99; 8192 x 4096: 51, 55, 60 us).
+// CU, all resident (bf16 8192 x 8192: 92 us; 128 workgroups 137, 512 96; 8192 x
+// 4096: 50, 70, 53; 8 ranks' 625 x 2049: 23, 32, 26).
 constexpr int kNormBackMaxBlocks = 256;
 
 // Partial rows of dweight for one rank's rows (the same for every type, so

@@ -198,13 +198,14 @@ int ar_destroy(ar_comm_t comm);
  * 4-byte accumulators for the ring's hand-off (used by bfloat16 and by an
  * in-place all-reduce; otherwise a segment's running value is handed on
  * through its owner's row of recv), LL lines for the tree and the ring-LL
- * path, per-chunk ready flags for the pipelined ring, and a small control
- * block (LL epoch, flag base, error word).  The caller allocates at least
+ * path, per-chunk ready flags for the pipelined ring, a small control
+ * block (LL epoch, flag base, error word), and the gradient norm's partial
+ * sums and counters.  The caller allocates at least
  * this many bytes (any 256-byte aligned device allocation). */
 size_t ar_workspace_bytes(ar_comm_t comm);
 
-/* Hand the workspace to the communicator and clear its control block and
- * LL lines (enqueued on `stream`; ordered before any later call on the same
+/* Hand the workspace to the communicator and clear its control block, LL
+ * lines and the gradient norm's counters (enqueued on `stream`; ordered before any later call on the same
  * stream).  No page defines this call: it is this library's own boundary
  * design; the stream argument lets the clearing be ordered with the caller's
  * own work instead of synchronizing the device.  The memory stays owned by
@@ -503,7 +504,7 @@ typedef struct {
  * added in 64-bit floats, in an order that depends on sizes and the device
  * alone: no overflow or underflow in the sum, whatever the elements.  An
  * infinity or NaN among them gives that.  n == 0, or only empty tensors: 0.
- * Uses the comm's workspace (6.2 KiB of partial sums and counters at its
+ * Uses the comm's workspace (6.1 KiB of partial sums and counters at its
  * end), so it is ordered with the comm's collectives as they are with each
  * other. */
 int ar_grad_norm(ar_comm_t comm, const ar_span_t* grads, size_t n, float* norm, void* stream);
