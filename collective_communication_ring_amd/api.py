@@ -33,6 +33,12 @@ AR_SUM, AR_MAX, AR_MIN, AR_AVG = 0, 1, 2, 3
 COST_FORMS = {"tree-ll": AR_COST_TREE_LL, "ring-fused": AR_COST_RING_FUSED,
               "ring-pipelined": AR_COST_RING_PIPELINED, "ring-step": AR_COST_RING_STEP,
               "ring-ll": AR_COST_RING_LL, "tree-fused": AR_COST_TREE_FUSED}
+AR_ROTARY_HALVES, AR_ROTARY_PAIRS = 0, 1
+(AR_SCALING_NONE, AR_SCALING_LINEAR, AR_SCALING_BASE, AR_SCALING_BANDS,
+ AR_SCALING_RAMP) = range(5)
+ROTARY_LAYOUTS = {"halves": AR_ROTARY_HALVES, "pairs": AR_ROTARY_PAIRS}
+SCALINGS = {None: AR_SCALING_NONE, "linear": AR_SCALING_LINEAR, "base": AR_SCALING_BASE,
+            "bands": AR_SCALING_BANDS, "ramp": AR_SCALING_RAMP}
 REDOPS = {"sum": AR_SUM, "max": AR_MAX, "min": AR_MIN, "avg": AR_AVG}
 
 DTYPES = {"int32": AR_INT32, "float32": AR_FLOAT32, "bf16": AR_BF16}
@@ -70,6 +76,54 @@ class ar_rmsnorm_backward_t(ctypes.Structure):
                 ("dsum", ctypes.c_void_p), ("dsum_stride", ctypes.c_size_t),
                 ("dx", ctypes.c_void_p), ("dx_stride", ctypes.c_size_t),
                 ("dweight", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class ar_rotary_scheme_t(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_size_t), ("scaling", ctypes.c_int)] + [
+        (n, ctypes.c_double) for n in ("base", "scale", "original", "low", "high", "fast", "slow")]
+
+
+class ar_rotation_t(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_size_t), ("layout", ctypes.c_int), ("factor", ctypes.c_float),
+                ("frequencies", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("position_bytes", ctypes.c_int), ("position_stride", ctypes.c_size_t)]
+
+
+class ar_heads_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_size_t),
+                ("token_stride", ctypes.c_size_t), ("head_stride", ctypes.c_size_t)]
+
+
+_HEAD_SIZES = [(n, ctypes.c_size_t) for n in ("batch", "tokens", "q_heads", "k_heads", "dim")]
+
+
+class ar_rotary_t(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("inverse", ctypes.c_int)] + _HEAD_SIZES + [
+        ("rotation", ar_rotation_t)] + [(n, ar_heads_t) for n in ("q", "k", "q_out", "k_out")]
+
+
+class ar_head_rmsnorm_t(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float)] + _HEAD_SIZES + [("rotation", ar_rotation_t)] + [
+        (n, ar_heads_t) for n in ("q", "k", "q_out", "k_out")] + [
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class ar_head_rmsnorm_backward_t(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("ranks", ctypes.c_int),
+                ("eps", ctypes.c_float)] + _HEAD_SIZES + [("rotation", ar_rotation_t)] + [
+        (n, ar_heads_t) for n in ("dq_out", "dk_out", "q", "k", "dq", "dk")] + [
+        (n, ctypes.c_void_p) for n in ("q_weight", "k_weight", "q_dweight", "k_dweight", "workspace")
+    ] + [("workspace_bytes", ctypes.c_size_t)]
+
+
+class ar_orthogonalize_t(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("steps", ctypes.c_int), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("count", ctypes.c_size_t), ("rows", ctypes.c_size_t),
+                ("cols", ctypes.c_size_t), ("x", ctypes.POINTER(ctypes.c_void_p)),
+                ("x_stride", ctypes.c_size_t), ("out", ctypes.POINTER(ctypes.c_void_p)),
+                ("out_stride", ctypes.c_size_t), ("coefficients", ctypes.POINTER(ctypes.c_float)),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
@@ -123,6 +177,15 @@ def lib():
         "ar_grad_norm": ([vp, ctypes.POINTER(ar_span_t), sz, vp, vp], i),
         "ar_grad_clip": ([ctypes.POINTER(ar_span_t), ctypes.POINTER(ar_span_t), sz, vp,
                           ctypes.c_float, vp], i),
+        "ar_rotary_frequencies": ([ctypes.POINTER(ar_rotary_scheme_t),
+                                   ctypes.POINTER(ctypes.c_double),
+                                   ctypes.POINTER(ctypes.c_double)], i),
+        "ar_rotary": ([ctypes.POINTER(ar_rotary_t), vp], i),
+        "ar_head_rmsnorm": ([ctypes.POINTER(ar_head_rmsnorm_t), vp], i),
+        "ar_head_rmsnorm_backward": ([ctypes.POINTER(ar_head_rmsnorm_backward_t), vp], i),
+        "ar_head_rmsnorm_backward_workspace": ([i, sz], sz),
+        "ar_orthogonalize": ([ctypes.POINTER(ar_orthogonalize_t), vp], i),
+        "ar_orthogonalize_workspace": ([sz, sz, sz], sz),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -296,6 +359,46 @@ def ar_grad_clip(spans, out_spans, n, norm_ptr, max_norm, stream=0):
     _ok(lib().ar_grad_clip(spans, out_spans, n, norm_ptr, max_norm, stream), "ar_grad_clip")
 
 
+def ar_rotary_frequencies(scheme):
+    """scheme: an ar_rotary_scheme_t.  (frequencies, a list of rot_dim / 2
+    radians a position, and the factor)"""
+    f = (ctypes.c_double * max(1, scheme.rot_dim // 2))()
+    factor = ctypes.c_double()
+    _ok(lib().ar_rotary_frequencies(ctypes.byref(scheme), f, ctypes.byref(factor)),
+        "ar_rotary_frequencies")
+    return list(f), factor.value
+
+
+def ar_rotary(args, stream=0):
+    """args: an ar_rotary_t."""
+    _ok(lib().ar_rotary(ctypes.byref(args), stream), "ar_rotary")
+
+
+def ar_head_rmsnorm(args, stream=0):
+    """args: an ar_head_rmsnorm_t."""
+    _ok(lib().ar_head_rmsnorm(ctypes.byref(args), stream), "ar_head_rmsnorm")
+
+
+def ar_head_rmsnorm_backward(args, stream=0):
+    """args: an ar_head_rmsnorm_backward_t."""
+    _ok(lib().ar_head_rmsnorm_backward(ctypes.byref(args), stream), "ar_head_rmsnorm_backward")
+
+
+def ar_head_rmsnorm_backward_workspace(ranks, dim):
+    """Bytes; 0 for sizes that ar_head_rmsnorm_backward refuses."""
+    return lib().ar_head_rmsnorm_backward_workspace(ranks, dim)
+
+
+def ar_orthogonalize(args, stream=0):
+    """args: an ar_orthogonalize_t."""
+    _ok(lib().ar_orthogonalize(ctypes.byref(args), stream), "ar_orthogonalize")
+
+
+def ar_orthogonalize_workspace(count, rows, cols):
+    """Bytes; 0 for sizes that ar_orthogonalize refuses, or for nothing."""
+    return lib().ar_orthogonalize_workspace(count, rows, cols)
+
+
 # ---- torch convenience wrapper ---------------------------------------------
 
 def _torch_dtype(dt):
@@ -318,7 +421,8 @@ def binding():
         raise RuntimeError("_binding.so is not built (in %s); run __graft_entry__.build()" % HERE)
     from . import _binding
     _binding.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-                    (L.ar_rmsnorm, L.ar_reduce_scatter_rmsnorm, L.ar_rmsnorm_backward)))
+                    (L.ar_rmsnorm, L.ar_reduce_scatter_rmsnorm, L.ar_rmsnorm_backward, L.ar_rotary,
+                     L.ar_head_rmsnorm, L.ar_head_rmsnorm_backward, L.ar_orthogonalize)))
     _bound = (_binding, L)
     return _binding
 
@@ -362,6 +466,17 @@ def rmsnorm(x, weight, y, eps=1e-6, residual=None, sum=None, scale=None, group=0
     return y
 
 
+def _own_workspace(stream, make, *sizes):
+    """A workspace that a call makes for itself."""
+    if stream is None:
+        return make(*sizes)
+    # from that stream's memory: what was freed on the current one may still be
+    # in use there
+    import torch
+    with torch.cuda.stream(stream):
+        return make(*sizes)
+
+
 def rmsnorm_backward_workspace(ranks, rows, cols, device="cuda"):
     """A workspace for ``rmsnorm_backward`` calls of these sizes (a tensor the
     caller keeps; one call at a time may use it)."""
@@ -378,20 +493,149 @@ def rmsnorm_backward(dy, x, weight, rstd, dx, dweight, dsum=None, workspace=None
     ``ranks`` equal shards of the rows.  dx may be dy, x or dsum.  Without
     ``workspace`` (``rmsnorm_backward_workspace``) one is allocated."""
     if workspace is None:
-        size = dweight.shape[0], x.shape[0], x.shape[-1], x.device
-        if stream is None:
-            workspace = rmsnorm_backward_workspace(*size)
-        else:
-            # from that stream's memory: what was freed on the current one may
-            # still be in use there
-            import torch
-            with torch.cuda.stream(stream):
-                workspace = rmsnorm_backward_workspace(*size)
+        workspace = _own_workspace(stream, rmsnorm_backward_workspace, dweight.shape[0], x.shape[0],
+                                   x.shape[-1], x.device)
     rc = (_bound and _bound[0] or binding()).rmsnorm_backward(
         dy, x, weight, rstd, dx, dweight, dsum, workspace, _stream_of(x, stream))
     if rc:
         raise ArError(rc, "ar_rmsnorm_backward")
     return dx
+
+
+class Rotation:
+    """How heads are rotated by their tokens' positions: the first ``rot_dim``
+    elements of each, in pairs (i, i + rot_dim / 2) (layout "halves") or (2i, 2i
+    + 1) ("pairs"), pair i by base^(-2i / rot_dim) radians a position.
+
+    scaling, for contexts ``scale`` times the ``original`` length: None,
+    "linear", "base", "bands" (with ``low`` and ``high``) or "ramp" (with
+    ``fast`` and ``slow``, and a ``factor`` of the rotated values), as ar.h's
+    AR_SCALING_* define them.  ``frequencies`` is a float64 tensor [rot_dim / 2]
+    on the device; it and ``factor`` may be given other values."""
+
+    def __init__(self, rot_dim, base=10000.0, layout="halves", scaling=None, scale=1.0, original=0,
+                 low=1.0, high=4.0, fast=32.0, slow=1.0, device="cuda"):
+        import torch
+        if scaling not in SCALINGS:
+            raise ValueError("scaling must be one of %s, got %r" % (list(SCALINGS), scaling))
+        if layout not in ROTARY_LAYOUTS:
+            raise ValueError("layout must be one of %s, got %r" % (list(ROTARY_LAYOUTS), layout))
+        frequencies, self.factor = ar_rotary_frequencies(ar_rotary_scheme_t(
+            rot_dim, SCALINGS[scaling], base, scale, original, low, high, fast, slow))
+        self.layout = ROTARY_LAYOUTS[layout]
+        self.frequencies = torch.tensor(frequencies, dtype=torch.float64, device=device)
+
+
+def rotary(q, positions, rotation, q_out, k=None, k_out=None, inverse=False, stream=None):
+    """Rotates heads by their tokens' positions (``ar_rotary``): q [batch,
+    tokens, heads, dim] or [tokens, heads, dim], float32 or bfloat16, any
+    distances between batches, tokens and heads (``x.transpose(1, 2)`` of heads
+    ahead of tokens), to ``q_out``, and k (with a head count of its own) to
+    ``k_out``.  positions: int32 or int64, [batch, tokens], or [tokens] for all
+    batches.  ``rotation``: a ``Rotation``.  inverse: the transpose, for the
+    outputs' gradients in the backward pass.  Outputs may be their inputs."""
+    rc = (_bound and _bound[0] or binding()).rotary(
+        q, q_out, k, k_out, positions, rotation.frequencies, rotation.layout, rotation.factor,
+        bool(inverse), _stream_of(q, stream))
+    if rc:
+        raise ArError(rc, "ar_rotary")
+    return q_out
+
+
+def _turn(positions, rotation):
+    if rotation is None:
+        return positions, None, 0, 1.0
+    return positions, rotation.frequencies, rotation.layout, rotation.factor
+
+
+def head_rmsnorm(q, q_weight, q_out, eps=1e-6, k=None, k_weight=None, k_out=None, positions=None,
+                 rotation=None, stream=None):
+    """RMS norm of each head of q, by ``q_weight`` [dim], and of k, by
+    ``k_weight``, and with ``positions`` and ``rotation`` the rotation of what
+    comes out (``ar_head_rmsnorm``).  Arrays as ``rotary``'s; the weights are of
+    their type or float32.  Outputs may be their inputs."""
+    rc = (_bound and _bound[0] or binding()).head_rmsnorm(
+        q, q_weight, q_out, eps, k, k_weight, k_out, *_turn(positions, rotation),
+        _stream_of(q, stream))
+    if rc:
+        raise ArError(rc, "ar_head_rmsnorm")
+    return q_out
+
+
+def head_rmsnorm_backward_workspace(ranks, dim, device="cuda"):
+    """A workspace for ``head_rmsnorm_backward`` calls of these sizes (a tensor
+    the caller keeps; one call at a time may use it)."""
+    import torch
+    return torch.empty(max(256, ar_head_rmsnorm_backward_workspace(ranks, dim)), dtype=torch.uint8,
+                       device=device)
+
+
+def head_rmsnorm_backward(dq_out, q, q_weight, dq, q_dweight, eps=1e-6, dk_out=None, k=None,
+                          k_weight=None, dk=None, k_dweight=None, positions=None, rotation=None,
+                          workspace=None, stream=None):
+    """Backward pass of ``head_rmsnorm`` (``ar_head_rmsnorm_backward``): from
+    the outputs' gradients and the forward's inputs, dq and dk, and the weights'
+    gradients [ranks, dim] float32, a row for each of ``ranks`` equal shards of
+    the batches.  dq may be dq_out or q, dk dk_out or k.  Without ``workspace``
+    (``head_rmsnorm_backward_workspace``) one is allocated."""
+    if workspace is None:
+        workspace = _own_workspace(stream, head_rmsnorm_backward_workspace, q_dweight.shape[0],
+                                   q.shape[-1], q.device)
+    rc = (_bound and _bound[0] or binding()).head_rmsnorm_backward(
+        dq_out, q, q_weight, dq, q_dweight, eps, dk_out, k, k_weight, dk, k_dweight,
+        *_turn(positions, rotation), workspace, _stream_of(q, stream))
+    if rc:
+        raise ArError(rc, "ar_head_rmsnorm_backward")
+    return dq
+
+
+# Newton-Schulz coefficients that take singular values of 0.002 and more to
+# about 0.7 .. 1.2 in five steps.
+ORTHOGONALIZE_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize_workspace(count, rows, cols, dtype=None, device="cuda"):
+    """A workspace for ``orthogonalize`` calls of ``count`` matrices (a tensor
+    the caller keeps; one call at a time may use it; its size is the same for
+    every dtype)."""
+    import torch
+    return torch.empty(max(256, ar_orthogonalize_workspace(count, rows, cols)), dtype=torch.uint8,
+                       device=device)
+
+
+def orthogonalize(x, y, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7, scale=1.0,
+                  workspace=None, stream=None):
+    """Orthogonalises matrices of one shape by Newton-Schulz steps
+    (``ar_orthogonalize``): X = x / (norm(x) + eps), ``steps`` times X = a X +
+    (b A + c A^2) X with A = X X^T, and scale * X to ``y``.
+
+    x, y: float32 or bfloat16, [rows, cols], [count, rows, cols], or a list of
+    [rows, cols] (rows equally far apart in all); y may be x.  coefficients:
+    (a, b, c), or three for each step.  Without ``workspace``
+    (``orthogonalize_workspace``) one is allocated; a smaller one, down to that
+    of one matrix, takes the matrices in parts."""
+    xs, ys = _matrices(x), _matrices(y)
+    if not xs and not ys:
+        return y
+    flat = [float(c) for row in coefficients for c in (row if hasattr(row, "__len__") else (row,))]
+    if len(flat) == 3:
+        flat = flat * steps
+    if len(flat) != 3 * steps:
+        raise ValueError("coefficients must be three, or three for each of %d steps" % steps)
+    if workspace is None:
+        workspace = _own_workspace(stream, orthogonalize_workspace, len(xs), xs[0].shape[0],
+                                   xs[0].shape[-1], xs[0].dtype, xs[0].device)
+    rc = (_bound and _bound[0] or binding()).orthogonalize(xs, ys, flat, eps, scale, workspace,
+                                                           _stream_of(xs[0], stream))
+    if rc:
+        raise ArError(rc, "ar_orthogonalize")
+    return y
+
+
+def _matrices(x):
+    if isinstance(x, (list, tuple)):
+        return list(x)
+    return [x] if x.dim() == 2 else list(x.unbind(0))
 
 
 class TensorList:

@@ -23,7 +23,8 @@ LIB = os.path.join(HERE, "libar.so")
 BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["ar_comm.cpp", "ar_ring.hip", "ar_fused.hip", "ar_pipe.hip", "ar_ring_ll.hip", "ar_tree.hip",
            "ar_tree_fused.hip", "ar_util.hip", "ar_noalloc.hip", "ar_ops.cpp", "ar_norm.hip",
-           "ar_norm_back.hip", "ar_grad.hip"]
+           "ar_norm_back.hip", "ar_grad.hip", "ar_heads_host.cpp", "ar_heads.hip", "ar_heads_back.hip",
+           "ar_ortho_host.cpp", "ar_ortho.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

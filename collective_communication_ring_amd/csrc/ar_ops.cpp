@@ -7,20 +7,13 @@
 #include <iterator>
 #include <vector>
 
+#include "ar_checks.h"
 #include "ar_internal.h"
 #include "ar_ops.h"
 
 using namespace ar;
 
 namespace {
-
-constexpr size_t kMaxElems = (size_t)1 << 46;  // sizes above are refused: no byte offset wraps
-
-size_t size_of(int dtype) { return dtype == AR_E4M3 ? 1 : dtype == AR_BF16 ? 2 : 4; }
-
-bool stream_type(int dtype) { return dtype == AR_FLOAT32 || dtype == AR_BF16; }
-
-bool misaligned(const void* p, int dtype) { return (uintptr_t)p % size_of(dtype) != 0; }
 
 // An array of `rows` rows of `len` bytes, `stride` bytes apart.
 struct Rows {
@@ -79,14 +72,6 @@ bool bad_stride(size_t rows, size_t cols, size_t* stride)
     if (rows == 1)
         *stride = cols;
     return *stride < cols || *stride > kMaxElems / rows;
-}
-
-int done(hipError_t e)
-{
-    if (e == hipSuccess)
-        return AR_SUCCESS;
-    g_util_hip_error = (int)e;
-    return AR_ERR_HIP;
 }
 
 }  // namespace

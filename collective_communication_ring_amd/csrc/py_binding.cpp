@@ -7,9 +7,12 @@
 // library that the package has loaded.  Nothing is kept from call to call.
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <exception>
+#include <initializer_list>
 #include <string>
+#include <vector>
 
 #include "ar.h"
 
@@ -18,6 +21,10 @@ namespace {
 decltype(&ar_rmsnorm) p_rmsnorm = nullptr;
 decltype(&ar_reduce_scatter_rmsnorm) p_reduce_scatter_rmsnorm = nullptr;
 decltype(&ar_rmsnorm_backward) p_rmsnorm_backward = nullptr;
+decltype(&ar_rotary) p_rotary = nullptr;
+decltype(&ar_head_rmsnorm) p_head_rmsnorm = nullptr;
+decltype(&ar_head_rmsnorm_backward) p_head_rmsnorm_backward = nullptr;
+decltype(&ar_orthogonalize) p_orthogonalize = nullptr;
 
 // A refused argument: becomes a ValueError.
 struct Refused : std::exception {
@@ -208,12 +215,17 @@ void expect(Py_ssize_t got, Py_ssize_t want)
         throw Refused("the binding has not been given the library's entry points");
 }
 
-// init(ar_rmsnorm, ar_reduce_scatter_rmsnorm, ar_rmsnorm_backward): addresses.
+// init(ar_rmsnorm, ar_reduce_scatter_rmsnorm, ar_rmsnorm_backward, ar_rotary, ar_head_rmsnorm,
+// ar_head_rmsnorm_backward, ar_orthogonalize): addresses.
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
-        if (n != 3)
+        if (n != 7)
             throw Refused("wrong number of arguments");
+        p_rotary = reinterpret_cast<decltype(p_rotary)>(handle(a[3]));
+        p_head_rmsnorm = reinterpret_cast<decltype(p_head_rmsnorm)>(handle(a[4]));
+        p_head_rmsnorm_backward = reinterpret_cast<decltype(p_head_rmsnorm_backward)>(handle(a[5]));
+        p_orthogonalize = reinterpret_cast<decltype(p_orthogonalize)>(handle(a[6]));
         p_rmsnorm = reinterpret_cast<decltype(p_rmsnorm)>(handle(a[0]));
         p_reduce_scatter_rmsnorm = reinterpret_cast<decltype(p_reduce_scatter_rmsnorm)>(handle(a[1]));
         p_rmsnorm_backward = reinterpret_cast<decltype(p_rmsnorm_backward)>(handle(a[2]));
@@ -345,6 +357,257 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// ---- attention heads -----------------------------------------------------------
+
+// What a call's arrays of heads have in common: [batch, tokens, heads, dim], or
+// [tokens, heads, dim].
+struct HeadShape {
+    int64_t device, batch, tokens, dim;
+    at::ScalarType type;
+    bool three;
+};
+
+HeadShape head_shape(const at::Tensor& q, int* dtype)
+{
+    *dtype = code_of(q.scalar_type());
+    if (*dtype != AR_FLOAT32 && *dtype != AR_BF16)
+        throw Refused("q has dtype " + type_text(q.scalar_type()) +
+                      ": float32 or bfloat16 is wanted");
+    if (!q.is_cuda())
+        throw Refused("q must be on the GPU");
+    if (q.dim() != 3 && q.dim() != 4)
+        throw Refused("q must have shape ([batch,] tokens, heads, dim), got " + shape_text(q.sizes()));
+    const bool three = q.dim() == 3;
+    return {q.get_device(), three ? 1 : q.size(0), q.size(three ? 0 : 1), q.size(three ? 2 : 3),
+            q.scalar_type(), three};
+}
+
+// An array of `heads` heads (-1: as many as it has, which are returned).
+int64_t heads_of(const at::Tensor& t, const HeadShape& s, int64_t heads, const char* what,
+                 ar_heads_t* out)
+{
+    const int64_t d = s.three ? 3 : 4;
+    if (t.dim() == d && heads < 0)
+        heads = t.size(d - 2);
+    const int64_t four[] = {s.batch, s.tokens, heads, s.dim};
+    check(t, s.device, s.three ? at::IntArrayRef(four + 1, 3) : at::IntArrayRef(four, 4), s.type, what);
+    if (s.dim > 1 && t.stride(d - 1) != 1)
+        throw Refused(std::string("the last dimension of ") + what + " must be contiguous");
+    *out = {t.data_ptr(), s.three ? 0 : (size_t)t.stride(0), (size_t)t.stride(d - 3),
+            (size_t)t.stride(d - 2)};
+    return heads;
+}
+
+// positions, frequencies (None: no rotation), layout, factor
+void rotation_of(PyObject* const* a, const HeadShape& s, ar_rotation_t* r)
+{
+    const at::Tensor *positions = tensor_or_none(a[0], "positions"),
+                     *frequencies = tensor_or_none(a[1], "frequencies");
+    if (!frequencies && !positions)
+        return;
+    if (!frequencies || !positions)
+        throw Refused("a rotation needs positions and frequencies");
+    if (frequencies->dim() != 1)
+        throw Refused("frequencies must have shape (rot_dim / 2,), got " +
+                      shape_text(frequencies->sizes()));
+    r->frequencies = static_cast<const double*>(block_of(
+        *frequencies, s.device, frequencies->sizes(), at::kDouble, "the rotation's frequencies"));
+    r->rot_dim = 2 * (size_t)frequencies->size(0);
+    r->layout = (int)integer(a[2]);
+    r->factor = real(a[3]);
+    const at::ScalarType type = positions->scalar_type();
+    if (type != at::kInt && type != at::kLong)
+        throw Refused("positions have dtype " + type_text(type) + ": int32 or int64 is wanted");
+    r->position_bytes = type == at::kInt ? 4 : 8;
+    const bool shared = positions->dim() == 1;
+    const int64_t two[] = {s.batch, s.tokens};
+    check(*positions, s.device, shared ? at::IntArrayRef(two + 1, 1) : at::IntArrayRef(two, 2), type,
+          "positions");
+    if (s.tokens > 1 && positions->stride(shared ? 0 : 1) != 1)
+        throw Refused("the last dimension of positions must be contiguous");
+    r->positions = positions->data_ptr();
+    r->position_stride = shared || s.batch == 1 ? 0 : (size_t)positions->stride(0);
+}
+
+const void* head_weight(PyObject* o, const HeadShape& s, const char* what, int* weight_dtype)
+{
+    const at::Tensor& w = tensor(o, what);
+    const int code = code_of(w.scalar_type());
+    if ((code != AR_FLOAT32 && w.scalar_type() != s.type) || (*weight_dtype >= 0 && code != *weight_dtype))
+        throw Refused(std::string(what) + " has dtype " + type_text(w.scalar_type()) + ": " +
+                      (*weight_dtype >= 0 ? "that of q_weight" : type_text(s.type) + " or torch.float32") +
+                      " is wanted");
+    *weight_dtype = code;
+    return block_of(w, s.device, {s.dim}, w.scalar_type(), what);
+}
+
+// The keys' arguments come all together or not at all.
+bool all_or_none(PyObject* const* a, std::initializer_list<int> which, const char* names)
+{
+    int given = 0;
+    for (int i : which)
+        given += a[i] != Py_None;
+    if (given && given != (int)which.size())
+        throw Refused(std::string("the keys need all of ") + names);
+    return given;
+}
+
+// rotary(q, q_out, k, k_out, positions, frequencies, layout, factor, inverse, stream) -> status
+PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        expect(n, 10);
+        ar_rotary_t p = {};
+        const at::Tensor& q = tensor(a[0], "q");
+        const HeadShape s = head_shape(q, &p.dtype);
+        p.batch = (size_t)s.batch;
+        p.tokens = (size_t)s.tokens;
+        p.dim = (size_t)s.dim;
+        p.q_heads = (size_t)heads_of(q, s, -1, "q", &p.q);
+        heads_of(tensor(a[1], "q_out"), s, (int64_t)p.q_heads, "q_out", &p.q_out);
+        if (all_or_none(a, {2, 3}, "k and k_out")) {
+            p.k_heads = (size_t)heads_of(tensor(a[2], "k"), s, -1, "k", &p.k);
+            heads_of(tensor(a[3], "k_out"), s, (int64_t)p.k_heads, "k_out", &p.k_out);
+        }
+        rotation_of(a + 4, s, &p.rotation);
+        p.inverse = (int)integer(a[8]);
+        return status_of(p_rotary, &p, handle(a[9]));
+    });
+}
+
+// head_rmsnorm(q, q_weight, q_out, eps, k, k_weight, k_out, positions, frequencies, layout, factor,
+// stream) -> status
+PyObject* head_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        expect(n, 12);
+        ar_head_rmsnorm_t p = {};
+        const at::Tensor& q = tensor(a[0], "q");
+        const HeadShape s = head_shape(q, &p.dtype);
+        p.weight_dtype = -1;
+        p.eps = real(a[3]);
+        p.batch = (size_t)s.batch;
+        p.tokens = (size_t)s.tokens;
+        p.dim = (size_t)s.dim;
+        p.q_heads = (size_t)heads_of(q, s, -1, "q", &p.q);
+        p.q_weight = head_weight(a[1], s, "q_weight", &p.weight_dtype);
+        heads_of(tensor(a[2], "q_out"), s, (int64_t)p.q_heads, "q_out", &p.q_out);
+        if (all_or_none(a, {4, 5, 6}, "k, k_weight and k_out")) {
+            p.k_heads = (size_t)heads_of(tensor(a[4], "k"), s, -1, "k", &p.k);
+            p.k_weight = head_weight(a[5], s, "k_weight", &p.weight_dtype);
+            heads_of(tensor(a[6], "k_out"), s, (int64_t)p.k_heads, "k_out", &p.k_out);
+        }
+        rotation_of(a + 7, s, &p.rotation);
+        return status_of(p_head_rmsnorm, &p, handle(a[11]));
+    });
+}
+
+// head_rmsnorm_backward(dq_out, q, q_weight, dq, q_dweight, eps, dk_out, k, k_weight, dk, k_dweight,
+// positions, frequencies, layout, factor, workspace, stream) -> status
+PyObject* head_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        expect(n, 17);
+        ar_head_rmsnorm_backward_t p = {};
+        const at::Tensor &q = tensor(a[1], "q"), &q_dweight = tensor(a[4], "q_dweight"),
+                         &workspace = tensor(a[15], "workspace");
+        const HeadShape s = head_shape(q, &p.dtype);
+        if (q_dweight.dim() != 2)
+            throw Refused("q_dweight must have shape (ranks, dim), got " + shape_text(q_dweight.sizes()));
+        const int64_t ranks = q_dweight.size(0), shape[] = {ranks, s.dim};
+        if (ranks < 1 || s.batch % ranks)
+            throw Refused(std::to_string(s.batch) + " batches are not " + std::to_string(ranks) +
+                          " equal shards");
+        p.ranks = ranks > 1 << 20 ? 1 << 20 : (int)ranks;  // refused all the same
+        p.weight_dtype = -1;
+        p.eps = real(a[5]);
+        p.batch = (size_t)s.batch;
+        p.tokens = (size_t)s.tokens;
+        p.dim = (size_t)s.dim;
+        p.q_heads = (size_t)heads_of(q, s, -1, "q", &p.q);
+        heads_of(tensor(a[0], "dq_out"), s, (int64_t)p.q_heads, "dq_out", &p.dq_out);
+        heads_of(tensor(a[3], "dq"), s, (int64_t)p.q_heads, "dq", &p.dq);
+        p.q_weight = head_weight(a[2], s, "q_weight", &p.weight_dtype);
+        p.q_dweight = static_cast<float*>(block_of(q_dweight, s.device, shape, at::kFloat, "q_dweight"));
+        if (all_or_none(a, {6, 7, 8, 9, 10}, "dk_out, k, k_weight, dk and k_dweight")) {
+            p.k_heads = (size_t)heads_of(tensor(a[7], "k"), s, -1, "k", &p.k);
+            heads_of(tensor(a[6], "dk_out"), s, (int64_t)p.k_heads, "dk_out", &p.dk_out);
+            heads_of(tensor(a[9], "dk"), s, (int64_t)p.k_heads, "dk", &p.dk);
+            p.k_weight = head_weight(a[8], s, "k_weight", &p.weight_dtype);
+            p.k_dweight = static_cast<float*>(
+                block_of(tensor(a[10], "k_dweight"), s.device, shape, at::kFloat, "k_dweight"));
+        }
+        rotation_of(a + 11, s, &p.rotation);
+        if (!workspace.is_cuda() || workspace.get_device() != s.device || !workspace.is_contiguous())
+            throw Refused("workspace must be a contiguous tensor on cuda:" + std::to_string(s.device));
+        p.workspace = workspace.data_ptr();
+        p.workspace_bytes = (size_t)workspace.nbytes();
+        return status_of(p_head_rmsnorm_backward, &p, handle(a[16]));
+    });
+}
+
+// orthogonalize(x, y, coefficients, eps, scale, workspace, stream) -> status; x and y are lists of
+// matrices, or one of [count, rows, cols] each; coefficients a list of 3 numbers for each step
+PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        expect(n, 7);
+        if (!PyList_Check(a[0]) || !PyList_Check(a[1]) || !PyList_Check(a[2]))
+            throw Refused("wrong arguments");
+        const Py_ssize_t count = PyList_GET_SIZE(a[0]);
+        if (!count || PyList_GET_SIZE(a[1]) != count)
+            throw Refused("x and y must be as many matrices, one at least");
+        ar_orthogonalize_t p = {};
+        const at::Tensor &x0 = tensor(PyList_GET_ITEM(a[0], 0), "x"),
+                         &y0 = tensor(PyList_GET_ITEM(a[1], 0), "y"), &workspace = tensor(a[5], "workspace");
+        const at::ScalarType type = x0.scalar_type();
+        p.dtype = code_of(type);
+        if (p.dtype != AR_FLOAT32 && p.dtype != AR_BF16)
+            throw Refused("x has dtype " + type_text(type) + ": float32 or bfloat16 is wanted");
+        if (!x0.is_cuda())
+            throw Refused("x must be on the GPU");
+        if (x0.dim() != 2 || y0.dim() != 2)
+            throw Refused("a matrix must have shape (rows, cols), got " +
+                          shape_text(x0.dim() != 2 ? x0.sizes() : y0.sizes()));
+        const int64_t dev = x0.get_device(), rows = x0.size(0), cols = x0.size(1);
+        const int64_t shape[] = {rows, cols};
+        std::vector<const void*> x((size_t)count);
+        std::vector<void*> y((size_t)count);
+        const auto matrix = [&](PyObject* o, const char* what, size_t* stride, Py_ssize_t i) {
+            size_t own = 0;
+            void* at = rows_of(tensor(o, what), dev, shape, type, what, &own);
+            if (i && rows > 1 && own != *stride)
+                throw Refused(std::string("the rows of all of ") + what + " must be equally far apart");
+            *stride = own;
+            return at;
+        };
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            x[(size_t)i] = matrix(PyList_GET_ITEM(a[0], i), "x", &p.x_stride, i);
+            y[(size_t)i] = matrix(PyList_GET_ITEM(a[1], i), "y", &p.out_stride, i);
+        }
+        const Py_ssize_t numbers = PyList_GET_SIZE(a[2]);
+        if (numbers % 3)
+            throw Refused("each step has three coefficients");
+        std::vector<float> coefficients((size_t)numbers);
+        for (Py_ssize_t i = 0; i < numbers; ++i)
+            coefficients[(size_t)i] = real(PyList_GET_ITEM(a[2], i));
+        if (!workspace.is_cuda() || workspace.get_device() != dev || !workspace.is_contiguous())
+            throw Refused("workspace must be a contiguous tensor on cuda:" + std::to_string(dev));
+        p.steps = (int)std::min<Py_ssize_t>(numbers / 3, 1 << 20);
+        p.eps = real(a[3]);
+        p.scale = real(a[4]);
+        p.count = (size_t)count;
+        p.rows = (size_t)rows;
+        p.cols = (size_t)cols;
+        p.x = x.data();
+        p.out = y.data();
+        p.coefficients = coefficients.data();
+        p.workspace = workspace.data_ptr();
+        p.workspace_bytes = (size_t)workspace.nbytes();
+        return status_of(p_orthogonalize, &p, handle(a[6]));
+    });
+}
+
 // Whether a tensor's elements fill one block of memory, in any order of its
 // dimensions: smallest stride first, each is the product of the sizes before.
 bool dense(const at::Tensor& t) { return t.is_non_overlapping_and_dense(); }
@@ -411,7 +674,9 @@ PyObject* is_dense(PyObject*, PyObject* const* a, Py_ssize_t n)
 
 #define METHOD(f) {#f, (PyCFunction)(void*)f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(init), METHOD(rmsnorm), METHOD(reduce_scatter_rmsnorm),
-                         METHOD(rmsnorm_backward), METHOD(spans), METHOD(same_layout),
+                         METHOD(rmsnorm_backward), METHOD(rotary), METHOD(head_rmsnorm),
+                         METHOD(head_rmsnorm_backward), METHOD(orthogonalize), METHOD(spans),
+                         METHOD(same_layout),
                          {"dense", (PyCFunction)(void*)is_dense, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,

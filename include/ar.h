@@ -520,6 +520,178 @@ int ar_grad_norm(ar_comm_t comm, const ar_span_t* grads, size_t n, float* norm, 
 int ar_grad_clip(const ar_span_t* grads, const ar_span_t* out, size_t n, const float* norm,
                  float max_norm, void* stream);
 
+/* ---- Operators on attention heads ------------------------------------------
+ * What stands between a rank's product for queries and keys and its attention.
+ * Heads are arrays [batch][tokens][heads][dim] with any distances between
+ * batches, tokens and heads (so also [batch][heads][tokens][dim] in memory,
+ * or a part of the rows that one product wrote for queries, keys and values);
+ * the dim elements of a head are contiguous.  Logical ranks are batches: each
+ * rank's own heads behind one another.  Queries and keys go in one call and
+ * one launch; either may have no heads.  Conventions are those of the
+ * operators above. */
+
+/* Which elements of a head's first rot_dim are a pair: i and i + rot_dim / 2,
+ * or 2i and 2i + 1. */
+typedef enum { AR_ROTARY_HALVES = 0, AR_ROTARY_PAIRS = 1 } ar_rotary_layout_t;
+
+/* Pair i turns by frequency f_i = base^(-2i / rot_dim) radians a position.
+ * Scaled for contexts `scale` (>= 1) times the `original` length:
+ *   LINEAR  f / scale
+ *   BASE    base grows to base * scale^(rot_dim / (rot_dim - 2)), which leaves
+ *           the fastest pair as it is and divides the slowest by scale
+ *   BANDS   pairs that turn at least `high` times over the original length
+ *           stay, those that turn at most `low` times are divided by scale,
+ *           between them f (k + (1 - k) / scale), k = (turns - low) / (high - low)
+ *   RAMP    the same from pair `lo` to pair `hi`, linear in the pair's number:
+ *           f (1 - k + k / scale), k = clamp((i - lo) / (hi - lo), 0, 1), with
+ *           lo = max(floor(at(fast)), 0), hi = min(ceil(at(slow)), rot_dim - 1),
+ *           at(t) = rot_dim ln(original / (2 pi t)) / (2 ln base) the pair that
+ *           turns t times over the original length (hi - lo at least 0.001);
+ *           rotated values are multiplied by 0.1 ln(scale) + 1 */
+typedef enum {
+    AR_SCALING_NONE = 0,
+    AR_SCALING_LINEAR = 1,
+    AR_SCALING_BASE = 2,
+    AR_SCALING_BANDS = 3,
+    AR_SCALING_RAMP = 4
+} ar_rotary_scaling_t;
+typedef struct {
+    size_t rot_dim;   /* even, 2 .. 1024 (BASE: from 4) */
+    int scaling;      /* AR_SCALING_* */
+    double base;      /* > 1, finite */
+    double scale;     /* >= 1, finite; ignored for NONE */
+    double original;  /* > 0, finite; BANDS and RAMP */
+    double low, high; /* 0 < low < high; BANDS */
+    double fast, slow; /* 0 < slow < fast; RAMP */
+} ar_rotary_scheme_t;
+/* Frequencies of a scheme to `frequencies` [rot_dim / 2], HOST memory, and the
+ * factor of rotated values (1 but for RAMP) to *factor. */
+int ar_rotary_frequencies(const ar_rotary_scheme_t* scheme, double* frequencies, double* factor);
+
+/* A rotation of heads: pair (a, b) of a token at position p becomes
+ *   (c a - s b, c b + s a),  c = factor cos(p f_i), s = factor sin(p f_i),
+ * elements from rot_dim on stay.  p f_i is taken and reduced in 64 bits, c and
+ * s are float32.  Positions are any integers, also negative ones. */
+typedef struct {
+    size_t rot_dim;            /* even, at most dim; 0: no rotation */
+    int layout;                /* AR_ROTARY_* */
+    float factor;              /* finite */
+    const double* frequencies; /* device, [rot_dim / 2] radians a position */
+    const void* positions;     /* device, [batch][tokens] integers */
+    int position_bytes;        /* 4 or 8 */
+    size_t position_stride;    /* from one batch to the next; 0: all have the same */
+} ar_rotation_t;
+
+/* An array of heads: distances in elements. */
+typedef struct {
+    void* data;
+    size_t batch_stride, token_stride, head_stride;
+} ar_heads_t;
+
+/* q_out = the rotation of q, k_out that of k; inverse != 0: its transpose,
+ * which the backward pass applies to the outputs' gradients (the inverse
+ * where factor is 1).  The arithmetic is float32, each output rounded once;
+ * elements that are not rotated are copied.  q_out may be q's array
+ * and k_out k's (same address, distances); any other overlap of an output is
+ * AR_ERR_INVALID_USAGE, and an output's distances must nest (each at least
+ * what the next smaller one spans), else AR_ERR_INVALID_ARG.  Arrays that lie
+ * in turn in one array, with the same distances, do not overlap.
+ * batch * tokens * (q_heads + k_heads) is below 2^31, dim at most 1024; none
+ * of batches, tokens or heads is a successful no-op. */
+typedef struct {
+    int dtype; /* AR_FLOAT32 or AR_BF16 */
+    int inverse;
+    size_t batch, tokens, q_heads, k_heads, dim;
+    ar_rotation_t rotation; /* rot_dim >= 2 */
+    ar_heads_t q, k, q_out, k_out;
+} ar_rotary_t;
+int ar_rotary(const ar_rotary_t* args, void* stream);
+
+/* RMS norm of each head, and the rotation of what comes out: for each head x
+ *   r = 1 / sqrt(mean(x * x) + eps),  v = x * r * weight,  out = rotation of v
+ * with q_weight [dim] for all heads of q, k_weight for those of k.  r and v
+ * are float32, each output is rounded once.  Sums of squares are float32;
+ * where they leave its range they are taken again in 64 bits.  Overlaps and
+ * sizes as ar_rotary's; rotation.rot_dim may be 0 (a norm alone). */
+typedef struct {
+    int dtype;        /* AR_FLOAT32 or AR_BF16: q, k, q_out, k_out */
+    int weight_dtype; /* dtype, or AR_FLOAT32 */
+    float eps;        /* finite, >= 0 */
+    size_t batch, tokens, q_heads, k_heads, dim;
+    ar_rotation_t rotation;
+    ar_heads_t q, k, q_out, k_out;
+    const void *q_weight, *k_weight;
+} ar_head_rmsnorm_t;
+int ar_head_rmsnorm(const ar_head_rmsnorm_t* args, void* stream);
+
+/* Its backward pass.  With u the rotation's transpose of dq_out, n = q r (r
+ * taken again from q) and g = u * q_weight, for each head
+ *   dq = r * (g - n * mean(g * n)),   q_dweight = sum over heads of u * n
+ * and the same for k.  The batches are `ranks` equal shards, one after the
+ * other (batch a multiple of ranks), and q_dweight, k_dweight are [ranks][dim]
+ * float32, a row for each rank's own heads.  Sums are float32, in an order
+ * that depends on sizes alone.  dq may be dq_out's or q's array, dk dk_out's
+ * or k's; other overlaps as above.  `workspace` is
+ * ar_head_rmsnorm_backward_workspace bytes of device memory, 256-byte aligned,
+ * whose contents mean nothing between calls.  No tokens: zeros to q_dweight
+ * (q_heads > 0) and k_dweight (k_heads > 0). */
+typedef struct {
+    int dtype;
+    int weight_dtype;
+    int ranks; /* 1 .. 64 */
+    float eps;
+    size_t batch, tokens, q_heads, k_heads, dim;
+    ar_rotation_t rotation;
+    ar_heads_t dq_out, dk_out, q, k, dq, dk;
+    const void *q_weight, *k_weight;
+    float *q_dweight, *k_dweight;
+    void* workspace;
+    size_t workspace_bytes;
+} ar_head_rmsnorm_backward_t;
+int ar_head_rmsnorm_backward(const ar_head_rmsnorm_backward_t* args, void* stream);
+size_t ar_head_rmsnorm_backward_workspace(int ranks, size_t dim); /* 0 for sizes it refuses */
+
+/* ---- An update of orthogonal directions ---------------------------------------
+ * Newton-Schulz steps on `count` matrices of one shape: what an optimiser
+ * makes of a reduced and clipped gradient, or of its momentum.  For each x
+ * [rows][cols]
+ *   X = x / (norm(x) + eps), norm the root of the sum of squares;
+ *   `steps` times, with (a, b, c) = coefficients[step]:
+ *       A = X X^T,  X = a X + (b A + c A A) X     (rows > cols: X^T X, from the right)
+ *   out = scale * X
+ * Every product is held to about float32's accuracy: X, A and b A + c A A are
+ * kept as two 16-bit floats each (22 significant bits), and their products are
+ * three matrix products of those with float32 sums; the norm's sum is 64-bit.
+ * A matrix of zeros gives zeros (eps > 0); one with an infinity or NaN gives
+ * NaN.
+ * x and out are HOST arrays of device addresses, read during the call only;
+ * rows of a matrix are x_stride (out_stride) elements apart.  out[i] may be
+ * x[i] (with the same stride); other overlaps, also of different matrices, are
+ * AR_ERR_INVALID_USAGE.  coefficients: HOST memory, [steps][3], finite; steps
+ * that can take a singular value (0 to 1 at first) past 2^16 by a s + b s^3 +
+ * c s^5 are AR_ERR_UNSUPPORTED.
+ * rows, cols <= 65536; steps 1 .. 64.  count, rows or cols of 0 is a
+ * successful no-op.  `workspace` is ar_orthogonalize_workspace bytes of device
+ * memory, 256-byte aligned, whose contents mean nothing between calls; a
+ * smaller one of at least the bytes for one matrix is used for one part of
+ * the matrices after another. */
+typedef struct {
+    int dtype; /* AR_FLOAT32 or AR_BF16: x, out */
+    int steps;
+    float eps;   /* finite, >= 0 */
+    float scale; /* finite */
+    size_t count, rows, cols;
+    const void* const* x;
+    size_t x_stride;
+    void* const* out;
+    size_t out_stride;
+    const float* coefficients;
+    void* workspace;
+    size_t workspace_bytes;
+} ar_orthogonalize_t;
+int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream);
+size_t ar_orthogonalize_workspace(size_t count, size_t rows, size_t cols); /* 0 for sizes it refuses */
+
 /* Message for a status code (static storage).  No page defines this call:
  * it is this library's own boundary design. */
 const char* ar_status_string(int status);
@@ -527,7 +699,8 @@ const char* ar_status_string(int status);
 /* Last hipError_t seen by this comm (0 if none); with comm == NULL, the last
  * one seen by the calling thread's utility calls (ar_stream_*,
  * ar_ll_pingpong) and calls without a comm (ar_rmsnorm, ar_rmsnorm_backward,
- * ar_grad_clip). */
+ * ar_grad_clip, ar_rotary, ar_head_rmsnorm, ar_head_rmsnorm_backward,
+ * ar_orthogonalize). */
 int ar_last_hip_error(ar_comm_t comm);
 
 #ifdef __cplusplus
