@@ -15,24 +15,31 @@ namespace ar {
 // 2^e and lo that of what is left, 22 significant bits of the two.  The host
 // keeps e such that no value of the matrix passes 2^14; below it the bits of a
 // value end at 2^-24, 2^-38 of the largest, so a matrix's error stays near
-// 2^-23 of its norm however its values spread.  A row is cut into pieces of 32
-// columns, 32 hi and then 32 lo: the 128 bytes that one row gives to one step
-// of a product.  Columns are padded with zeros to whole pieces.
+// 2^-23 of its norm however its values spread.
+//
+// It is kept in pieces of 32 columns, piece by piece: 128 bytes a row, 32 hi and
+// then 32 lo, all rows of a piece behind one another, so that what a tile's
+// rows give to one step of a product is one stretch of memory.  (Row by row, the
+// steps of a tile's rows lie at a distance that is often a power of two, all in
+// one channel of an L2.)
+// Columns are padded with zeros to whole pieces.
 constexpr uint32_t kPiece = 32;
 constexpr uint32_t padded(uint32_t n) { return (n + kPiece - 1) / kPiece * kPiece; }
 constexpr int kOrthoTop = 14;
 
 constexpr int kOrthoBatch = 128;  // matrices of one round of launches, at most
-constexpr int kNormParts = 64;    // partial sums of a matrix's norm
+constexpr int kNormParts = 512;   // partial sums of a matrix's norm, at most
 
 struct OrthoPointers {
     const void* p[kOrthoBatch];
 };
 
 struct OrthoSplitArgs {
-    double* parts;        // [count][kNormParts]
-    _Float16* rowwise;    // [rows][2 padded(cols)], a matrix's `each` halves behind the last one's
-    _Float16* colwise;    // [cols][2 padded(rows)]
+    double* parts;        // [count][kNormParts], of which nparts are in use (set by the launch)
+    uint32_t nparts;
+    _Float16* rowwise;    // x, a matrix's `each` halves behind the last one's
+    _Float16* colwise;    // its transpose
+    uint32_t* tickets;    // kOrthoTickets, zeroed
     uint64_t each;
     uint64_t stride;      // of x
     uint32_t rows, cols;
@@ -41,21 +48,35 @@ struct OrthoSplitArgs {
     double up;            // 2^e
 };
 
-// C = s_acc P Q^T + s_add D, P [m][K], Q [n][K], D and C [m][n], all in halves
-// (s_acc and s_add hold the exponents too).
+// C = s_acc P Q^T + s_add D, P [m][K], Q [n][K], all in halves (s_acc and s_add
+// hold the exponents too).
 struct OrthoProductArgs {
-    const _Float16 *p, *q, *d;  // d may be NULL
-    _Float16* c;                // [m][2 padded(n)], or NULL
-    _Float16* ct;               // [n][2 padded(m)], its transpose; or NULL
-    uint64_t each_p, each_q, each_d, each_c, each_ct;  // from one matrix to the next
+    const _Float16 *p, *q;
+    const _Float16* dt;         // D^T [n][m], or NULL
+    _Float16 *c, *ct;           // C [m][n] and its transpose
+    uint64_t each;              // from one matrix's arrays to the next one's
     uint32_t m, n, k;           // k: pieces
-    int symmetric;              // C is (m == n, c == ct): tiles below the diagonal only, each
+    int symmetric;              // C is (m == n, c == ct): tiles of the lower triangle only, each
                                 //   written to both its places
     float s_acc, s_add;
     // the last product: C goes to the caller's arrays instead, [m][n] or transposed
     int last, transposed, bf16;
     uint64_t out_stride;
+    // few tiles: each by `parts` workgroups, a part of the pieces each (set by the launch)
+    float* slots;               // [tile][part][its sums]
+    uint32_t* tickets;          // a tile's, zero between launches
+    uint32_t parts;
+    uint32_t tiles_m, tiles_n, tiles;  // of a matrix, down and across, and all that are made
 };
+
+// Products whose tiles (of this side) go by parts, of so many pieces at least:
+// workgroups and parts of a tile, at most; a slot holds a part's sums.
+constexpr uint32_t kOrthoPartPieces = 16;
+constexpr uint32_t kOrthoSlots = 256;
+constexpr uint32_t kOrthoTickets = 256;
+constexpr uint32_t kOrthoParts = 8;
+constexpr uint32_t kOrthoPartTile = 64;
+constexpr size_t kOrthoSlotBytes = kOrthoPartTile * kOrthoPartTile * 4;
 
 hipError_t launch_ortho_split(const OrthoPointers& x, int count, const OrthoSplitArgs& a, hipStream_t s);
 hipError_t launch_ortho_product(const OrthoPointers& out, int count, const OrthoProductArgs& a,

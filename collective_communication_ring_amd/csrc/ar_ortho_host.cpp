@@ -78,11 +78,15 @@ int exponent(double most)
     return kOrthoTop - (most > 0.0 ? std::max(-100, std::ilogb(most) + 1) : -100);
 }
 
-struct Extent {
-    uintptr_t at, end;
-};
+// Bytes ahead of the matrices' arrays: the tickets and, where a side is long
+// enough for products to go by parts, their slots.
+size_t shared_bytes(const Layout& l)
+{
+    return kOrthoTickets * 4 +
+           (padded(l.n) >= kOrthoPartPieces * 2 * kPiece ? kOrthoSlots * kOrthoSlotBytes : 0);
+}
 
-// Matrices' extents; those of one stride may lie in turn.
+// Whether two matrices share a byte; rows of one stride may lie in turn.
 bool meet(uintptr_t x, uintptr_t y, uint64_t rows, uint64_t len, uint64_t step_x, uint64_t step_y)
 {
     if (x + (rows - 1) * step_x + len <= y || y + (rows - 1) * step_y + len <= x)
@@ -99,7 +103,8 @@ extern "C" size_t ar_orthogonalize_workspace(size_t count, size_t rows, size_t c
 {
     if (rows > kMaxSide || cols > kMaxSide || !count || !rows || !cols)
         return 0;
-    return layout_of(rows, cols).each * 2 * std::min<size_t>(count, kOrthoBatch);
+    const Layout l = layout_of(rows, cols);
+    return shared_bytes(l) + l.each * 2 * std::min<size_t>(count, kOrthoBatch);
 }
 
 extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
@@ -122,10 +127,11 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
         p.x_stride > kMaxElems / p.rows || p.out_stride > kMaxElems / p.rows)
         return AR_ERR_INVALID_ARG;
     const Layout l = layout_of(p.rows, p.cols);
-    const size_t room = std::min<size_t>(std::min<size_t>(p.workspace_bytes / (l.each * 2), p.count),
-                                         kOrthoBatch);
-    if (!p.workspace || !room || (uintptr_t)p.workspace % 256)
+    const size_t shared = shared_bytes(l);
+    if (!p.workspace || p.workspace_bytes < shared + l.each * 2 || (uintptr_t)p.workspace % 256)
         return AR_ERR_INVALID_ARG;
+    const size_t room = std::min<size_t>(
+        std::min<size_t>((p.workspace_bytes - shared) / (l.each * 2), p.count), kOrthoBatch);
     for (size_t i = 0; i < p.count; ++i)
         if (!p.x[i] || !p.out[i] || misaligned(p.x[i], p.dtype) || misaligned(p.out[i], p.dtype))
             return AR_ERR_INVALID_ARG;
@@ -152,7 +158,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
         }
         std::sort(items.begin(), items.end(), [](const Item& x, const Item& y) { return x.at < y.at; });
         const uint64_t reach_x = (p.rows - 1) * step_x + len, reach_out = (p.rows - 1) * step_out + len;
-        const uintptr_t ws = (uintptr_t)p.workspace, ws_end = ws + room * l.each * 2;
+        const uintptr_t ws = (uintptr_t)p.workspace, ws_end = ws + shared + room * l.each * 2;
         for (size_t i = 0; i < items.size(); ++i) {
             const Item& v = items[i];
             const uint64_t reach = v.out ? reach_out : reach_x;
@@ -184,7 +190,8 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
 
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool tall = p.rows > p.cols;
-    _Float16* const w = static_cast<_Float16*>(p.workspace);
+    _Float16* const w = static_cast<_Float16*>(p.workspace) + shared / 2;
+    uint32_t* const tickets = static_cast<uint32_t*>(p.workspace);
     for (size_t first = 0; first < p.count; first += room) {
         const int count = (int)std::min(room, p.count - first);
         OrthoPointers in{}, out{};
@@ -193,7 +200,8 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             out.p[i] = p.out[first + i];
         }
         OrthoSplitArgs split{};
-        split.parts = static_cast<double*>(p.workspace);
+        split.parts = reinterpret_cast<double*>(w);
+        split.tickets = tickets;
         split.rowwise = w + (tall ? l.xt[0] : l.x[0]);
         split.colwise = w + (tall ? l.x[0] : l.xt[0]);
         split.each = l.each;
@@ -209,7 +217,9 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             const int now = i & 1;
             const bool last = i + 1 == p.steps;
             OrthoProductArgs g{};
-            g.each_p = g.each_q = g.each_d = g.each_c = g.each_ct = l.each;
+            g.each = l.each;
+            g.tickets = tickets;
+            g.slots = reinterpret_cast<float*>(tickets + kOrthoTickets);
             g.bf16 = p.dtype == AR_BF16;
             // A = X X^T
             g.p = g.q = w + l.x[now];
@@ -222,7 +232,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             if (e != hipSuccess)
                 break;
             // B = b A + c A A
-            g.p = g.q = g.d = w + l.a;
+            g.p = g.q = g.dt = w + l.a;
             g.c = g.ct = w + l.b;
             g.k = padded(l.m) / kPiece;
             g.s_acc = (float)std::ldexp((double)k[2], eb[i] - 2 * ea[i]);
@@ -233,7 +243,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             // X = a X + B X
             g.p = w + l.b;
             g.q = w + l.xt[now];
-            g.d = w + l.x[now];
+            g.dt = w + l.xt[now];
             g.c = w + l.x[!now];
             g.ct = w + l.xt[!now];
             g.n = l.n;

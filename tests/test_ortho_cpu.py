@@ -84,7 +84,9 @@ def test_workspace(api):
     f = api.ar_orthogonalize_workspace
     assert f(0, 5, 5) == f(1, 0, 5) == f(1, 5, 0) == f(1, 65537, 5) == 0
     assert f(1, 100, 300) == f(1, 300, 100)
-    assert f(3, 100, 300) == 3 * f(1, 100, 300) and f(1, 1, 1) % 256 == 0
+    one = f(2, 100, 300) - f(1, 100, 300)
+    assert f(3, 100, 300) == f(1, 100, 300) + 2 * one and f(1, 1, 1) % 256 == 0
+    assert f(500, 100, 300) == f(128, 100, 300)  # more go by parts
 
 
 def test_wrapper_refuses(api):

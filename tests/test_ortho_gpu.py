@@ -109,6 +109,28 @@ def test_larger(env, m, n):
     _steps(env, m, n)
 
 
+@pytest.mark.parametrize("count,m,n,steps", [(1, 100, 2500, 2), (1, 2300, 70, 2), (1, 2900, 2900, 1),
+                                             (1, 4096, 4100, 1), (1, 4400, 4096, 1), (9, 1030, 1000, 2)])
+def test_every_tile(env, count, m, n, steps):
+    """Sizes at which each tile is taken for each product (64 to 256 wide, whole
+    and by parts), against the form computed on the GPU; with two steps, the
+    second from the first's result."""
+    torch, api, dev = env["torch"], env["api"], env["dev"]
+    g = torch.Generator(device=dev).manual_seed(m)
+    x = torch.randn(count, m, n, generator=g, device=dev) * 0.02
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    api.orthogonalize(x, y, 1, COEFFICIENTS, EPS)
+    if steps > 1:
+        api.orthogonalize(x, z, 2, COEFFICIENTS, EPS)
+    torch.cuda.synchronize()
+    for i in {0, count - 1}:
+        value, slack = of.one_step(x[i], COEFFICIENTS, EPS)
+        ob.between(y[i], value, slack, (m, n))
+        if steps > 1:
+            value, slack = of.next_step(y[i], 1, COEFFICIENTS)
+            ob.between(z[i], value, slack, (m, n, "second"))
+
+
 def test_values(env):
     """Few directions, wide ranges of values, the smallest and largest floats."""
     torch = env["torch"]
