@@ -360,13 +360,13 @@ def ar_grad_clip(spans, out_spans, n, norm_ptr, max_norm, stream=0):
 
 
 def ar_rotary_frequencies(scheme):
-    """scheme: an ar_rotary_scheme_t.  (frequencies, a list of rot_dim / 2
-    radians a position, and the factor)"""
+    """scheme: an ar_rotary_scheme_t.  (frequencies, a ctypes array of rot_dim /
+    2 radians a position, and the factor)"""
     f = (ctypes.c_double * max(1, scheme.rot_dim // 2))()
     factor = ctypes.c_double()
     _ok(lib().ar_rotary_frequencies(ctypes.byref(scheme), f, ctypes.byref(factor)),
         "ar_rotary_frequencies")
-    return list(f), factor.value
+    return f, factor.value
 
 
 def ar_rotary(args, stream=0):
@@ -523,7 +523,7 @@ class Rotation:
         frequencies, self.factor = ar_rotary_frequencies(ar_rotary_scheme_t(
             rot_dim, SCALINGS[scaling], base, scale, original, low, high, fast, slow))
         self.layout = ROTARY_LAYOUTS[layout]
-        self.frequencies = torch.tensor(frequencies, dtype=torch.float64, device=device)
+        self.frequencies = torch.frombuffer(frequencies, dtype=torch.float64).to(device)
 
 
 def rotary(q, positions, rotation, q_out, k=None, k_out=None, inverse=False, stream=None):

@@ -39,11 +39,10 @@ struct Turn {
     uint64_t position_stride;
     int wide;        // positions are 64-bit
     int layout;
-    uint32_t pairs;  // rot_dim / 2
-    uint32_t slots;  // pairs, rounded up to a vector's: the length of a token's table
+    uint32_t pairs;  // rot_dim / 2: 0 for no rotation
     float factor;
     float sign;      // -1: the transpose
-    FastDiv per_slot;
+    uint32_t lanes;  // that take a token's pairs: a power of two, 64 at most
 };
 
 struct HeadsArgs {
@@ -53,31 +52,45 @@ struct HeadsArgs {
     uint32_t rows;          // batch * tokens * heads
     FastDiv heads, tokens;  // of a token (both sides); of a batch
     uint32_t dim, nvec;     // elements and vectors of a head
-    uint32_t turned;        // units that are rotated
+    uint32_t turned;        // rotated units of a head, halves
     uint32_t lanes;         // threads per head
     uint32_t turns;         // heads a group of lanes takes, one after the other
-    float eps;
+    uint32_t table;         // cosines and sines of a wave's tokens, at most
+    float eps, per_dim;     // per_dim: 1 / dim
     int weight_f32;
     int stream;             // outputs larger than the L2s
     Turn turn;
 };
 
+// How a thread goes from one of its heads to the next: so many heads and tokens
+// on, or one token more where that passes a token's last head.
+struct HeadsStep {
+    uint32_t heads, tokens;
+    // elements that x, dy and dx are moved by, and further by with that token
+    uint64_t by[3], more[3];
+};
+
 struct HeadsBackArgs {
     HeadsArray dy[2], x[2], dx[2];
+    HeadsStep step[2];      // (set by the launch)
     const void* weight[2];
     float* dweight[2];      // [ranks][dim]
-    float* partial;         // [ranks][blocks of both sides][dim]
+    float* partial;         // [ranks][blocks][both sides][dim]
     uint32_t heads[2];
     FastDiv head[2];        // division by heads
     FastDiv tokens;
-    uint32_t rows[2];       // of one rank: heads of its batches
-    uint32_t rank_tokens;   // tokens of one rank, all its batches
+    uint32_t rank_batches, rank_tokens;  // of one rank: batches, and tokens of all of them
     uint32_t dim, nvec;
     uint32_t turned;
     uint32_t lanes;
     int ranks;
-    int blocks[2];          // workgroups per rank
-    float eps;
+    uint32_t blocks;        // workgroups per rank
+    uint32_t chunk;         // tokens whose angles are made at once, of one batch
+    uint32_t batch_chunks;  // chunks of a batch
+    uint32_t run;           // chunks of a wave
+    int apart;              // waves have queries and keys in turn, of one chunk
+    FastDiv chunks;         // division by batch_chunks
+    float eps, per_dim;
     int weight_f32;
     int stream;
     Turn turn;
@@ -86,14 +99,10 @@ struct HeadsBackArgs {
 constexpr uint32_t kHeadMaxDim = 1024;
 constexpr int kHeadPerLane = 16;  // elements of a head that a thread holds
 
-// Partial rows of the weights' gradients of all ranks and both sides, at most
-// (a rank has one at least for each side).
-constexpr int kHeadBackBlocks = 1024;
-inline int head_back_blocks(int ranks)
-{
-    const int b = kHeadBackBlocks / ranks;
-    return b < 2 ? 2 : b;
-}
+// Workgroups of the backward pass, at most: three on each CU, as its registers
+// allow for; each leaves a partial row of both weights' gradients.
+constexpr int kHeadBackBlocks = 768;
+inline int head_back_blocks(int ranks) { return kHeadBackBlocks / ranks; }
 
 // Elements of a vector: the widest of 16 bytes and less that divides a head,
 // and in the layout of halves the half that is rotated.

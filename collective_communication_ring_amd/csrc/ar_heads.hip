@@ -12,32 +12,30 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// A head lies in the registers of `lanes` threads, 16 elements each, two
-// vectors of a pair in one thread in both layouts, so the rotation needs no
-// exchange.  A workgroup takes `turns` rounds of 256 / lanes heads, of queries
-// and keys alike, token by token; cosines and sines are computed once for each
-// of its tokens, into LDS, while the first heads' loads are in flight.
-template <class E, int W, bool NORM, bool NT>
+// A head lies in the registers of `lanes` threads, 16 elements each, two vectors
+// of a pair in one thread in both layouts, so the rotation needs no exchange.  A
+// wave takes `turns` rounds of 64 / lanes heads, of queries and keys alike, token
+// by token, the next round's loads in flight; it computes cosines and sines once
+// for each of its tokens, into LDS of its own.
+template <class E, int W, bool NORM, int LAYOUT, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_heads(HeadsArgs a)
 {
-    using H = Head<E, W>;
+    using H = Head<E, W, LAYOUT, WHOLE>;
     using T = typename E::T;
     extern __shared__ float2 s_table[];
-    const uint32_t group = kThreads / a.lanes, sub = threadIdx.x / a.lanes;
-    const uint32_t lane = threadIdx.x - sub * a.lanes;
-    const uint32_t row0 = blockIdx.x * (group * a.turns);
-    const uint32_t rows = a.rows - row0 < group * a.turns ? a.rows - row0 : group * a.turns;
-    const uint32_t first = divide(row0, a.heads);
-    const uint32_t count = divide(row0 + rows - 1, a.heads) - first + 1;
-    const uint32_t end = divide(a.rows - 1, a.heads) + 1;
-    const int layout = a.turn.layout;
-
+    const uint32_t group = 64 / a.lanes, sub = (threadIdx.x & 63u) / a.lanes;
+    const uint32_t lane = (threadIdx.x & 63u) - sub * a.lanes;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t row0 = (blockIdx.x * (kThreads / 64) + wave) * (group * a.turns);
+    const uint32_t rows = row0 >= a.rows ? 0 : a.rows - row0 < group * a.turns ? a.rows - row0
+                                                                              : group * a.turns;
     struct At {
         uint32_t token, side, b, t, h;
     };
     const auto place = [&](uint32_t k) {
         const uint32_t i = k * group + sub;
-        const uint32_t row = row0 + (i < rows ? i : rows - 1);  // no thread without a head
+        // no thread without a head: the last one there is
+        const uint32_t row = i < rows ? row0 + i : rows ? row0 + rows - 1 : a.rows - 1;
         At o;
         o.token = divide(row, a.heads);
         o.h = row - o.token * a.heads.by;
@@ -54,62 +52,61 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadsArgs a)
 
     H cur;
     At at = place(0);
-    cur.load(address(a.x, at), lane, a.lanes, a.nvec, a.turned, layout);
+    cur.load(address(a.x, at), lane, a.lanes, a.nvec, a.turned);
     float* s_w = reinterpret_cast<float*>(s_table);
-    float2* table = s_table;
+    float2* table = s_table + wave * a.table;
+    Weights<E> weights;
     if constexpr (NORM) {
         table += a.dim;  // behind both weights
-        for (uint32_t c = threadIdx.x; c < a.dim; c += kThreads) {
-            s_w[c] = a.weight[0] ? weight_at<E>(a.weight[0], a.weight_f32, c) : 0.0f;
-            s_w[a.dim + c] = a.weight[1] ? weight_at<E>(a.weight[1], a.weight_f32, c) : 0.0f;
-        }
+        weights.load(a.weight, a.weight_f32, a.dim);
     }
-    if (a.turned)
-        fill_angles(a.turn, a.tokens, first, count, end, table);
-    __syncthreads();
-    for (uint32_t k = 0; k < a.turns && k * group < rows; ++k) {
-        const At here = at;
-        float v[kHeadPerLane];
-        cur.get(v, lane, a.lanes, a.nvec, a.turned, layout);
-        if (k + 1 < a.turns) {
-            at = place(k + 1);
-            cur.load(address(a.x, at), lane, a.lanes, a.nvec, a.turned, layout);
-        }
+    const uint32_t first = divide(row0, a.heads);
+    if (rows && a.turn.pairs)
+        fill_angles(a.turn, a.tokens, first, divide(row0 + rows - 1, a.heads) - first + 1, table);
+    if constexpr (NORM) {
+        weights.store(a.weight, a.weight_f32, a.dim, s_w);
+        __syncthreads();
+    }
+    if (!rows)
+        return;
+    const auto head = [&](const At& here, float (&v)[kHeadPerLane]) {
         if constexpr (NORM) {
-            const float r = head_rstd(v, a.lanes, a.dim, a.eps);
+            const float r = head_rstd(v, a.lanes, a.dim, a.per_dim, a.eps);
             const float* w = s_w + (here.side ? a.dim : 0);
-            H::each(lane, a.lanes, a.nvec, a.turned, layout,
-                    [&](int i, uint32_t c) { v[i] = v[i] * r * w[c]; });
+            H::each(lane, a.lanes, a.nvec, a.turned, [&](int i, uint32_t c) { v[i] = v[i] * r * w[c]; });
         }
-        if (a.turned)
-            H::turn(v, table + (here.token - first) * a.turn.slots, lane, a.lanes, a.turned,
-                    a.turn.pairs, layout);
-        if (k * group + sub < rows)
-            H::template put<NT>(address(a.y, here), v, lane, a.lanes, a.nvec, a.turned, layout);
+        if (a.turn.pairs)
+            H::turn(v, table + (here.token - first) * a.turn.pairs, lane, a.lanes, a.turned, a.turn.pairs);
+    };
+    float v[kHeadPerLane];
+    uint32_t k = 0;
+    for (; (k + 1) * group < rows; ++k) {  // every thread has a head, and the wave another round
+        const At here = at;
+        cur.get(v, lane, a.lanes, a.nvec, a.turned);
+        at = place(k + 1);
+        cur.load(address(a.x, at), lane, a.lanes, a.nvec, a.turned);
+        head(here, v);
+        H::put(address(a.y, here), v, lane, a.lanes, a.nvec, a.turned, a.stream);
     }
-}
-
-template <class E, int W, bool NORM>
-void launch_width(const HeadsArgs& a, size_t lds, uint32_t grid, hipStream_t s)
-{
-    if (a.stream)
-        hipLaunchKernelGGL((k_heads<E, W, NORM, true>), dim3(grid), dim3(kThreads), lds, s, a);
-    else
-        hipLaunchKernelGGL((k_heads<E, W, NORM, false>), dim3(grid), dim3(kThreads), lds, s, a);
+    cur.get(v, lane, a.lanes, a.nvec, a.turned);
+    head(at, v);
+    if (k * group + sub < rows)
+        H::put(address(a.y, at), v, lane, a.lanes, a.nvec, a.turned, a.stream);
 }
 
 template <class E, bool NORM>
 void launch_typed(int width, const HeadsArgs& a, size_t lds, uint32_t grid, hipStream_t s)
 {
-    if constexpr (E::VEC == 8)
-        if (width == 8)
-            return launch_width<E, 8, NORM>(a, lds, grid, s);
-    if (width == 4)
-        launch_width<E, 4, NORM>(a, lds, grid, s);
-    else if (width == 2)
-        launch_width<E, 2, NORM>(a, lds, grid, s);
-    else
-        launch_width<E, 1, NORM>(a, lds, grid, s);
+    with_width<E>(width, a.dim == a.lanes * kHeadPerLane, [&](auto w) {
+        constexpr int W = decltype(w)::value;
+        constexpr bool WHOLE = decltype(w)::whole;
+        if (a.turn.layout == AR_ROTARY_HALVES)
+            hipLaunchKernelGGL((k_heads<E, W, NORM, AR_ROTARY_HALVES, WHOLE>), dim3(grid), dim3(kThreads),
+                               lds, s, a);
+        else
+            hipLaunchKernelGGL((k_heads<E, W, NORM, AR_ROTARY_PAIRS, WHOLE>), dim3(grid), dim3(kThreads),
+                               lds, s, a);
+    });
 }
 
 }  // namespace
@@ -126,9 +123,9 @@ int heads_vector(int dtype, uint32_t dim, const Turn& t)
 void heads_fit(uint32_t dim, int w, uint32_t* nvec, uint32_t* turned, uint32_t* lanes, Turn* t)
 {
     *nvec = dim / w;
-    *turned = (t->pairs + w - 1) / w;
-    t->slots = *turned * w;
-    t->per_slot = fast_div(t->slots ? t->slots : 1);
+    *turned = t->layout == AR_ROTARY_HALVES ? t->pairs / w : 0;
+    for (t->lanes = 1; t->lanes < 64 && t->lanes < t->pairs;)
+        t->lanes *= 2;
     *lanes = 1;
     while (*lanes * kHeadPerLane < dim)
         *lanes *= 2;
@@ -138,23 +135,34 @@ hipError_t launch_heads(int dtype, bool norm, HeadsArgs a, hipStream_t s)
 {
     const int w = heads_vector(dtype, a.dim, a.turn);
     heads_fit(a.dim, w, &a.nvec, &a.turned, &a.lanes, &a.turn);
+    a.per_dim = 1.0f / (float)a.dim;
     a.stream = (uint64_t)a.rows * a.dim * (dtype == AR_BF16 ? 2 : 4) > kStreamBytes;
-    const uint32_t group = kThreads / a.lanes;
-    const auto lds = [&](uint32_t turns) {
-        const uint32_t n = group * turns, tokens = (n + a.heads.by - 2) / a.heads.by + 1;
-        return (size_t)tokens * a.turn.slots * sizeof(float2) + (norm ? 8 * (size_t)a.dim : 0);
+    const uint32_t group = 64 / a.lanes, waves = kThreads / 64;
+    const auto table = [&](uint32_t turns) {  // cosines and sines of a wave's tokens
+        return ((group * turns + a.heads.by - 2) / a.heads.by + 1) * a.turn.pairs;
     };
+    // Rounds of a wave: those of whole tokens, 4 at least, where enough waves are left
+    // to fill the chip (8 ranks' 2048 x 10 heads of 128: 19.9 us by 4 or 5 rounds, 22.1
+    // by 2, 25.0 by one, 23.0 by 10), else as many as leave enough.
     const uint32_t rounds = (a.rows + group - 1) / group;
-    a.turns = std::max(1u, std::min(4u, rounds / 2048));
-    while (a.turns > 1 && lds(a.turns) > 20480)
+    uint32_t tokens = group;  // whose heads fill rounds: group / gcd(group, heads), a power of two
+    while (tokens > 1 && tokens / 2 * a.heads.by % group == 0)
+        tokens /= 2;
+    const uint32_t whole = tokens * a.heads.by / group;
+    a.turns = whole < 4 ? (3 + whole) / whole * whole : whole;
+    if (a.turns > 8 || rounds / a.turns < 4096)
+        a.turns = std::max(1u, std::min(4u, rounds / 4096));
+    while (a.turns > 1 && table(a.turns) > 512)
         --a.turns;
-    const uint32_t grid = (rounds + a.turns - 1) / a.turns;
+    a.table = table(a.turns);
+    const size_t lds = waves * a.table * sizeof(float2) + (norm ? 8 * (size_t)a.dim : 0);
+    const uint32_t grid = (rounds + a.turns * waves - 1) / (a.turns * waves);
     if (dtype == AR_FLOAT32)
-        norm ? launch_typed<Elem<AR_FLOAT32>, true>(w, a, lds(a.turns), grid, s)
-             : launch_typed<Elem<AR_FLOAT32>, false>(w, a, lds(a.turns), grid, s);
+        norm ? launch_typed<Elem<AR_FLOAT32>, true>(w, a, lds, grid, s)
+             : launch_typed<Elem<AR_FLOAT32>, false>(w, a, lds, grid, s);
     else
-        norm ? launch_typed<Elem<AR_BF16>, true>(w, a, lds(a.turns), grid, s)
-             : launch_typed<Elem<AR_BF16>, false>(w, a, lds(a.turns), grid, s);
+        norm ? launch_typed<Elem<AR_BF16>, true>(w, a, lds, grid, s)
+             : launch_typed<Elem<AR_BF16>, false>(w, a, lds, grid, s);
     return hipGetLastError();
 }
 

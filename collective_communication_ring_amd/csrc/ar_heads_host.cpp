@@ -345,7 +345,7 @@ extern "C" size_t ar_head_rmsnorm_backward_workspace(int ranks, size_t dim)
 {
     if (ranks < 1 || ranks > kMaxRanks || dim < 1 || dim > kHeadMaxDim)
         return 0;
-    return ((size_t)ranks * head_back_blocks(ranks) * dim * 4 + 255) / 256 * 256;
+    return ((size_t)ranks * head_back_blocks(ranks) * 2 * dim * 4 + 255) / 256 * 256;
 }
 
 extern "C" int ar_head_rmsnorm_backward(const ar_head_rmsnorm_backward_t* p, void* stream)
@@ -399,9 +399,8 @@ extern "C" int ar_head_rmsnorm_backward(const ar_head_rmsnorm_backward_t* p, voi
     a.dx[1] = array_of(p->dk);
     a.partial = static_cast<float*>(p->workspace);
     a.tokens = fast_div(s.tokens ? (uint32_t)s.tokens : 1);
-    a.rank_tokens = (uint32_t)(s.batch / (size_t)p->ranks * s.tokens);
-    for (int side = 0; side < 2; ++side)
-        a.rows[side] = a.rank_tokens * a.heads[side];
+    a.rank_batches = (uint32_t)(s.batch / (size_t)p->ranks);
+    a.rank_tokens = (uint32_t)(a.rank_batches * s.tokens);
     a.dim = (uint32_t)s.dim;
     a.ranks = p->ranks;
     a.eps = p->eps;
