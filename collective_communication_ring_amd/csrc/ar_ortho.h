@@ -48,8 +48,8 @@ struct OrthoSplitArgs {
     double up;            // 2^e
 };
 
-// C = s_acc P Q^T + s_add D, P [m][K], Q [n][K], all in halves (s_acc and s_add
-// hold the exponents too).
+// C = s_acc P Q^T + s_add D + diag I, P [m][K], Q [n][K], all in halves (the
+// factors hold the exponents too).
 struct OrthoProductArgs {
     const _Float16 *p, *q;
     const _Float16* dt;         // D^T [n][m], or NULL
@@ -58,7 +58,7 @@ struct OrthoProductArgs {
     uint32_t m, n, k;           // k: pieces
     int symmetric;              // C is (m == n, c == ct): tiles of the lower triangle only, each
                                 //   written to both its places
-    float s_acc, s_add;
+    float s_acc, s_add, diag;
     // the last product: C goes to the caller's arrays instead, [m][n] or transposed
     int last, transposed, bf16;
     uint64_t out_stride;
@@ -78,6 +78,32 @@ constexpr uint32_t kOrthoParts = 8;
 constexpr uint32_t kOrthoPartTile = 64;
 constexpr size_t kOrthoSlotBytes = kOrthoPartTile * kOrthoPartTile * 4;
 
+// A small matrix goes through all its steps in one workgroup's LDS: X, its
+// transpose, and one array for A and then B, whole 32 x 32 blocks of them, a block
+// to each of 16 waves.
+constexpr size_t kOrthoSmallBytes = 163584;  // and 256 bytes of sums: a CU's 160 KiB
+inline bool ortho_small(uint32_t m, uint32_t n)
+{
+    const uint64_t mp = padded(m), np = padded(n);
+    return mp * np <= 16 * 32 * 32 && (mp * np * 2 + mp * mp) * 4 <= kOrthoSmallBytes;
+}
+
+constexpr int kOrthoMaxSteps = 64;
+
+struct OrthoSmallArgs {
+    uint64_t x_stride, out_stride;
+    uint32_t rows, cols;
+    int bf16, steps;
+    float eps;
+    double up;  // 2^e of the first X
+    // a step's factors: A's, those of A A and A in B, of B X and X in X
+    struct {
+        float a, b_acc, b_add, x_acc, x_add;
+    } step[kOrthoMaxSteps];
+};
+
+hipError_t launch_ortho_small(const OrthoPointers& x, const OrthoPointers& out, int count,
+                              const OrthoSmallArgs& a, hipStream_t s);
 hipError_t launch_ortho_split(const OrthoPointers& x, int count, const OrthoSplitArgs& a, hipStream_t s);
 hipError_t launch_ortho_product(const OrthoPointers& out, int count, const OrthoProductArgs& a,
                                 hipStream_t s);

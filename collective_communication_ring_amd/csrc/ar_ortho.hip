@@ -222,11 +222,10 @@ __device__ inline void transpose4(uint32_t (&w)[4])
     }
 }
 
-// Values [i, i + 4) of column j to the caller's array.
-__device__ inline void store_out(void* to, const OrthoProductArgs& a, uint64_t at, uint32_t n,
-                                 const float (&v)[4])
+// Four values, or the first n of them, to the caller's array.
+__device__ inline void store_out(void* to, int bf16, uint64_t at, uint32_t n, const float (&v)[4])
 {
-    if (a.bf16) {
+    if (bf16) {
         uint16_t* o = static_cast<uint16_t*>(to) + at;
         if (n >= 4) {
             typedef uint32_t u32x2 __attribute__((ext_vector_type(2), aligned(2)));
@@ -255,7 +254,7 @@ __device__ inline void store_out(void* to, const OrthoProductArgs& a, uint64_t a
     }
 }
 
-// C = s_acc P Q^T + s_add D by tiles of B x B, a wave WM x WN of them in 32 x
+// C = s_acc P Q^T + s_add D + diag I by tiles of B x B, a wave WM x WN of them in 32 x
 // 32 products: lo hi + hi lo + hi hi for each 32 columns (lo lo is below 2^-22
 // of their product).  While a piece is multiplied, the next S - 1 are on their
 // way to LDS, by copies that need no registers.
@@ -543,13 +542,14 @@ __global__ __launch_bounds__(64 * (B / WM) * (B / WN)) void k_ortho_product(Orth
                     v[r] = g.acc[x][y][4 * r4 + r] * a.s_acc;
                     if (dt)
                         v[r] = fmaf((float)dh[r] + (float)dl[r], a.s_add, v[r]);
+                    v[r] += i + r == j ? a.diag : 0.0f;
                     v[r] = i + r < a.m && j < a.n ? v[r] : 0.0f;
                 }
                 uint32_t w[4];
                 if (a.last) {
                     if (a.transposed) {
                         if (j < a.n && i < a.m)
-                            store_out(to, a, j * a.out_stride + i, a.m - i, v);
+                            store_out(to, a.bf16, j * a.out_stride + i, a.m - i, v);
                     } else {
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
@@ -559,7 +559,7 @@ __global__ __launch_bounds__(64 * (B / WM) * (B / WN)) void k_ortho_product(Orth
                         for (int r = 0; r < 4; ++r)
                             v[r] = __uint_as_float(w[r]);
                         if (iq < a.m && jq < a.n)
-                            store_out(to, a, iq * a.out_stride + jq, a.n - jq, v);
+                            store_out(to, a.bf16, iq * a.out_stride + jq, a.n - jq, v);
                     }
                     continue;
                 }
@@ -593,7 +593,239 @@ __global__ __launch_bounds__(64 * (B / WM) * (B / WN)) void k_ortho_product(Orth
     });
 }
 
+// ---- small matrices ------------------------------------------------------------
+
+constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+
+// Place, in halves, of the hi half of (r, c) in a matrix of `rows` rows in LDS: its
+// pieces one after the other, the 16-byte chunks of a row exchanged as Stage's.
+__device__ inline uint32_t small_at(uint32_t r, uint32_t c, uint32_t rows, uint32_t low)
+{
+    return (c / kPiece * rows + r) * (2 * kPiece) + ((c % kPiece / 8 + 4 * low) ^ r / 2 % 8) * 8 + c % 8;
+}
+
+// One tile: rows i0 .. of p by rows j0 .. of q, k columns (a multiple of 32).  Two
+// sums of products, of which one need not wait for the other.
+__device__ inline f32x16 small_tile(const _Float16* p, uint32_t p_rows, uint32_t i0, const _Float16* q,
+                                    uint32_t q_rows, uint32_t j0, uint32_t k, uint32_t lane)
+{
+    f32x16 acc, low;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        acc[i] = low[i] = 0.0f;
+    const uint32_t i = i0 + lane % 32, j = j0 + lane % 32;
+#pragma unroll 1
+    for (uint32_t c0 = 0; c0 < k; c0 += 32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t c = c0 + 16 * h + lane / 32 * 8;
+            const auto at = [&](const _Float16* s, uint32_t r, uint32_t rows, uint32_t lower) {
+                return *reinterpret_cast<const f16x8*>(s + small_at(r, c, rows, lower));
+            };
+            const f16x8 ph = at(p, i, p_rows, 0), qh = at(q, j, q_rows, 0);
+            const f16x8 pl = at(p, i, p_rows, 1), ql = at(q, j, q_rows, 1);
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc, 0, 0, 0);
+            low = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, low, 0, 0, 0);
+            low = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, low, 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+        acc[r] += low[r];
+    return acc;
+}
+
+// Four consecutive values of a row, from column c on (a multiple of 4).
+__device__ inline void small_store(_Float16* s, uint32_t r, uint32_t c, uint32_t rows, const float (&v)[4])
+{
+    f16x4 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        _Float16 h, l;
+        split(v[i], &h, &l);
+        hi[i] = h;
+        lo[i] = l;
+    }
+    *reinterpret_cast<f16x4*>(s + small_at(r, c, rows, 0)) = hi;
+    *reinterpret_cast<f16x4*>(s + small_at(r, c, rows, 1)) = lo;
+}
+
+__device__ inline void small_load(const _Float16* s, uint32_t r, uint32_t c, uint32_t rows, float (&v)[4])
+{
+    const f16x4 hi = *reinterpret_cast<const f16x4*>(s + small_at(r, c, rows, 0));
+    const f16x4 lo = *reinterpret_cast<const f16x4*>(s + small_at(r, c, rows, 1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = (float)hi[i] + (float)lo[i];
+}
+
+// All steps of a matrix by one workgroup, 16 waves, a block of a product each: what
+// a product makes stays in registers until all waves have read what it replaces.
+// 160 x 96, five steps: 41 us, and 91 by a launch a product.
+template <class E>
+__global__ __launch_bounds__(kSmallThreads) void k_ortho_small(OrthoPointers in, OrthoPointers out,
+                                                               OrthoSmallArgs a)
+{
+    __shared__ _Float16 s_all[kOrthoSmallBytes / 2];
+    __shared__ double s_f[kSmallWaves];
+    const typename E::T* p = static_cast<const typename E::T*>(in.p[blockIdx.x]);
+    void* to = const_cast<void*>(out.p[blockIdx.x]);
+    const bool tall = a.rows > a.cols;
+    const uint32_t m = tall ? a.cols : a.rows, n = tall ? a.rows : a.cols;
+    const uint32_t mp = padded(m), np = padded(n);
+    _Float16 *x = s_all, *xt = x + 2 * mp * np, *ab = xt + 2 * mp * np;
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+
+    // the matrix, four columns of a row at a time, rows of four neighbouring threads
+    // one below the other
+    constexpr int kHeld = 4;
+    const uint32_t rp = padded(a.rows), cp = padded(a.cols), held = rp * cp / 4;
+    float v[kHeld][4];
+    double sum = 0.0;
+    each_of<kHeld>([&](auto g) {
+        const uint32_t i = g.value * kSmallThreads + threadIdx.x;
+        const uint32_t r = i / cp * 4 + i % 4, c = i % cp / 4 * 4;
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            v[g.value][z] = i < held && r < a.rows && c + z < a.cols ? E::widen(p[r * a.x_stride + c + z])
+                                                                     : 0.0f;
+    });
+    each_of<kHeld>([&](auto g) {
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            sum = fma((double)v[g.value][z], (double)v[g.value][z], sum);
+    });
+    const double up = a.up / (sqrt(block_sum<kSmallWaves>(sum, s_f)) + (double)a.eps);
+    each_of<kHeld>([&](auto g) {
+        const uint32_t i = g.value * kSmallThreads + threadIdx.x;
+        const uint32_t r = i / cp * 4, c = i % cp / 4 * 4;
+        uint32_t w[4];
+        float (&u)[4] = v[g.value];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            u[z] = (float)((double)u[z] * up);
+            w[z] = __float_as_uint(u[z]);
+        }
+        transpose4(w);
+        if (i < held) {
+            small_store(tall ? xt : x, r + i % 4, c, rp, u);
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                u[z] = __uint_as_float(w[z]);
+            small_store(tall ? x : xt, c + i % 4, r, cp, u);
+        }
+    });
+    __syncthreads();
+
+    // this wave's block of A and B, and of X
+    const uint32_t mt = mp / 32, nt = np / 32, ai = wave / mt * 32, aj = wave % mt * 32;
+    const uint32_t xi = wave / nt * 32, xj = wave % nt * 32;
+    const bool has_a = wave < mt * mt, has_x = wave < mt * nt;
+    f32x16 acc;
+    // f(g, i, j): four consecutive values of C^T's row j, from column i on, are acc[4 g ..]
+    const auto values = [&](uint32_t i0, uint32_t j0, auto f) {
+        each_of<4>([&](auto g) {
+            f(g, i0 + 8 * g.value + 4 * (lane / 32), j0 + lane % 32);
+        });
+    };
+    for (int step = 0;; ++step) {
+        const auto k = a.step[step];
+        if (has_a) {  // A = X X^T; A is its own transpose
+            acc = small_tile(x, mp, ai, x, mp, aj, np, lane);
+            values(ai, aj, [&](auto g, uint32_t i, uint32_t j) {
+                float u[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    u[r] = acc[4 * g.value + r] * k.a;
+                small_store(ab, j, i, mp, u);
+            });
+        }
+        __syncthreads();
+        if (has_a) {
+            acc = small_tile(ab, mp, ai, ab, mp, aj, mp, lane);
+            values(ai, aj, [&](auto g, uint32_t i, uint32_t j) {
+                float d[4];
+                small_load(ab, j, i, mp, d);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[4 * g.value + r] = fmaf(d[r], k.b_add, acc[4 * g.value + r] * k.b_acc);
+            });
+        }
+        __syncthreads();
+        if (has_a)
+            values(ai, aj, [&](auto g, uint32_t i, uint32_t j) {
+                const float u[4] = {acc[4 * g.value], acc[4 * g.value + 1], acc[4 * g.value + 2],
+                                    acc[4 * g.value + 3]};
+                small_store(ab, j, i, mp, u);
+            });
+        __syncthreads();
+        if (has_x) {
+            acc = small_tile(ab, mp, xi, xt, np, xj, mp, lane);
+            values(xi, xj, [&](auto g, uint32_t i, uint32_t j) {
+                float d[4];
+                small_load(xt, j, i, np, d);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[4 * g.value + r] = fmaf(d[r], k.x_add, acc[4 * g.value + r] * k.x_acc);
+            });
+        }
+        if (step + 1 == a.steps)
+            break;
+        __syncthreads();
+        if (has_x)
+            values(xi, xj, [&](auto g, uint32_t i, uint32_t j) {
+                float u[4];
+                uint32_t w[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    u[r] = acc[4 * g.value + r];
+                    w[r] = __float_as_uint(u[r]);
+                }
+                small_store(xt, j, i, np, u);
+                transpose4(w);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    u[r] = __uint_as_float(w[r]);
+                small_store(x, i + lane % 4, j & ~3u, mp, u);
+            });
+        __syncthreads();
+    }
+    if (has_x)
+        values(xi, xj, [&](auto g, uint32_t i, uint32_t j) {
+            float u[4];
+            uint32_t w[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                u[r] = acc[4 * g.value + r];
+                w[r] = __float_as_uint(u[r]);
+            }
+            if (tall) {
+                if (j < n && i < m)
+                    store_out(to, a.bf16, j * a.out_stride + i, m - i, u);
+                return;
+            }
+            transpose4(w);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                u[r] = __uint_as_float(w[r]);
+            const uint32_t iq = i + lane % 4, jq = j & ~3u;
+            if (iq < m && jq < n)
+                store_out(to, a.bf16, iq * a.out_stride + jq, n - jq, u);
+        });
+}
+
 }  // namespace
+
+hipError_t launch_ortho_small(const OrthoPointers& x, const OrthoPointers& out, int count,
+                              const OrthoSmallArgs& a, hipStream_t s)
+{
+    if (a.bf16)
+        hipLaunchKernelGGL(k_ortho_small<Elem<AR_BF16>>, dim3(count), dim3(kSmallThreads), 0, s, x, out, a);
+    else
+        hipLaunchKernelGGL(k_ortho_small<Elem<AR_FLOAT32>>, dim3(count), dim3(kSmallThreads), 0, s, x, out,
+                           a);
+    return hipGetLastError();
+}
 
 hipError_t launch_ortho_split(const OrthoPointers& x, int count, const OrthoSplitArgs& args, hipStream_t s)
 {

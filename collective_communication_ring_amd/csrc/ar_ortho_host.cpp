@@ -12,13 +12,29 @@ using namespace ar;
 namespace {
 
 constexpr size_t kMaxSide = 65536;
-constexpr int kMaxSteps = 64;
 
 // Where a matrix's arrays lie in the workspace, in halves; X [m][n] with m <= n.
 struct Layout {
     uint32_t m, n;
-    uint64_t x[2], xt[2], a, b, each;  // each: one matrix's, all arrays
+    bool merged;
+    uint64_t x[2], xt[2], square[5], each;  // each: one matrix's, all arrays
 };
+
+// Steps go by groups of up to three where the long side is this much the longer
+// one, and the matrix large: a group multiplies X twice, by its transpose and by
+// the product of the steps' polynomials, and does the rest on the short side's
+// square matrices.  A group of g saves 4 (g - 1) m^2 n operations, and makes 6
+// (g - 1) m^3 more, whose tiles fill the card better and write no transpose.  Five
+// steps, by groups and one by one, float32: 4096 x 5734 4.74 and 5.30 ms, 4096 x 8192
+// 5.39 and 6.42, 2048 x 4096 1127 and 1205 us, eight 1024 x 1433 1045 and 1102, but one
+// alone 260 and 253, 512 x 1024 177 and 170, 160 x 320 114 and 111.  (4096 x 8192 bfloat16, whose
+// groups may be larger: 4.91 ms.)  The number of matrices has no say, as the
+// workspace's layout is by the matrix.
+constexpr bool merges(uint32_t m, uint32_t n)
+{
+    return (uint64_t)n * 10 >= (uint64_t)m * 13 && (uint64_t)m * n >= 1u << 20;
+}
+constexpr int kMergeMost = 3;
 
 uint64_t whole(uint64_t halves) { return (halves + 127) / 128 * 128; }  // 256 bytes
 
@@ -38,9 +54,12 @@ Layout layout_of(size_t rows, size_t cols)
         *p = at;
         at += xt;
     }
-    l.a = at;
-    l.b = at + a;
-    l.each = l.b + a;
+    l.merged = merges(l.m, l.n);
+    for (int i = 0; i < (l.merged ? 5 : 2); ++i) {
+        l.square[i] = at;
+        at += a;
+    }
+    l.each = at;
     return l;
 }
 
@@ -70,6 +89,27 @@ double largest(const float* k, double top, bool whole_step)
         at(-b / (2.0 * c));
     }
     return most;
+}
+
+// Largest |f(s)| for s of [0, top], of polynomials of low degree: by samples, that
+// miss less than a hundredth of it (an exponent has room for three times).
+template <class F>
+double sampled(double top, F f)
+{
+    double most = 0.0;
+    for (int i = 0; i <= 256; ++i)
+        most = std::max(most, std::fabs(f(top * i / 256)));
+    return most;
+}
+
+double q_of(const float* k, double s) { return k[0] + s * s * (k[1] + s * s * k[2]); }
+
+// How much a step can widen an error of A = X X^T: the largest slope of s^2 -> p(s)^2.
+double widening(const float* k, double top)
+{
+    return sampled(top, [&](double s) {
+        return q_of(k, s) * (k[0] + s * s * (3.0 * k[1] + s * s * 5.0 * k[2]));
+    });
 }
 
 // The exponent that leaves values up to `most` at 2^kOrthoTop.
@@ -113,7 +153,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
         return AR_ERR_INVALID_ARG;
     ar_orthogonalize_t p = *args;
     if (!stream_type(p.dtype) || !(p.eps >= 0.0f) || std::isinf(p.eps) || !std::isfinite(p.scale) ||
-        p.steps < 1 || p.steps > kMaxSteps || p.rows > kMaxSide || p.cols > kMaxSide ||
+        p.steps < 1 || p.steps > kOrthoMaxSteps || p.rows > kMaxSide || p.cols > kMaxSide ||
         p.count > ((size_t)1 << 24) || !p.coefficients)
         return AR_ERR_INVALID_ARG;
     for (int i = 0; i < 3 * p.steps; ++i)
@@ -136,12 +176,14 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
         if (!p.x[i] || !p.out[i] || misaligned(p.x[i], p.dtype) || misaligned(p.out[i], p.dtype))
             return AR_ERR_INVALID_ARG;
 
-    // how large X and b A + c A A get, step by step: their exponents
+    // how large X and b A + c A A get, step by step, and their exponents
     std::vector<int> ex, eb, ea;
+    std::vector<double> tops;  // of X's singular values
     try {
         ex.resize(p.steps + 1);
         ea.resize(p.steps);
         eb.resize(p.steps);
+        tops.resize(p.steps + 1);
         const size_t z = size_of(p.dtype);
         const uint64_t len = p.cols * z, step_x = p.x_stride * z, step_out = p.out_stride * z;
         // out against everything, in order of address
@@ -177,17 +219,30 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
     } catch (...) {
         return AR_ERR_INTERNAL;
     }
-    double top = 1.0;  // of X's singular values
+    double top = tops[0] = 1.0;
     for (int i = 0; i < p.steps; ++i) {
         ex[i] = exponent(top);
         ea[i] = exponent(top * top);
         eb[i] = exponent(largest(p.coefficients + 3 * i, top, false));
-        top = largest(p.coefficients + 3 * i, top, true);
+        top = tops[i + 1] = largest(p.coefficients + 3 * i, top, true);
         if (!(top <= 65536.0))
             return AR_ERR_UNSUPPORTED;
     }
     ex[p.steps] = 0;
 
+    // what a step's sums and addends are multiplied by: coefficients, exponents, and
+    // in the end the scale
+    struct Factors {
+        float a, b_acc, b_add, x_acc, x_add;
+    };
+    const auto factors = [&](int i) {
+        const float* k = p.coefficients + 3 * i;
+        const double up = std::ldexp(i + 1 == p.steps ? (double)p.scale : 1.0, ex[i + 1] - ex[i]);
+        return Factors{(float)std::ldexp(1.0, ea[i] - 2 * ex[i]),
+                       (float)std::ldexp((double)k[2], eb[i] - 2 * ea[i]),
+                       (float)std::ldexp((double)k[1], eb[i] - ea[i]), (float)std::ldexp(up, -eb[i]),
+                       (float)((double)k[0] * up)};
+    };
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool tall = p.rows > p.cols;
     _Float16* const w = static_cast<_Float16*>(p.workspace) + shared / 2;
@@ -198,6 +253,25 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
         for (int i = 0; i < count; ++i) {
             in.p[i] = p.x[first + i];
             out.p[i] = p.out[first + i];
+        }
+        if (ortho_small(l.m, l.n)) {
+            OrthoSmallArgs a{};
+            a.x_stride = p.x_stride;
+            a.out_stride = p.out_stride;
+            a.rows = (uint32_t)p.rows;
+            a.cols = (uint32_t)p.cols;
+            a.bf16 = p.dtype == AR_BF16;
+            a.steps = p.steps;
+            a.eps = p.eps;
+            a.up = std::ldexp(1.0, ex[0]);
+            for (int i = 0; i < p.steps; ++i) {
+                const Factors f = factors(i);
+                a.step[i] = {f.a, f.b_acc, f.b_add, f.x_acc, f.x_add};
+            }
+            const hipError_t e = launch_ortho_small(in, out, count, a, s);
+            if (e != hipSuccess)
+                return done(e);
+            continue;
         }
         OrthoSplitArgs split{};
         split.parts = reinterpret_cast<double*>(w);
@@ -212,49 +286,105 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
         split.eps = p.eps;
         split.up = std::ldexp(1.0, ex[0]);
         hipError_t e = launch_ortho_split(in, count, split, s);
-        for (int i = 0; i < p.steps && e == hipSuccess; ++i) {
+        OrthoProductArgs g{};
+        g.each = l.each;
+        g.tickets = tickets;
+        g.slots = reinterpret_cast<float*>(tickets + kOrthoTickets);
+        g.bf16 = p.dtype == AR_BF16;
+        g.transposed = tall;
+        g.out_stride = p.out_stride;
+        // A symmetric product of square arrays: to = acc p q (+ add d + diag I)
+        const auto square = [&](const _Float16* x, const _Float16* y, const _Float16* d, uint64_t to,
+                                uint32_t pieces, double acc, double add, double diag) {
+            if (e != hipSuccess)
+                return;
+            OrthoProductArgs c = g;
+            c.p = x;
+            c.q = y;
+            c.dt = d;
+            c.c = c.ct = w + to;
+            c.m = c.n = l.m;
+            c.k = pieces;
+            c.symmetric = 1;
+            c.s_acc = (float)acc;
+            c.s_add = (float)add;
+            c.diag = (float)diag;
+            e = launch_ortho_product(out, count, c, s);
+        };
+        const uint32_t long_k = padded(l.n) / kPiece, short_k = padded(l.m) / kPiece;
+        const uint64_t A = l.square[0];
+        int now = 0;
+        for (int i = 0; i < p.steps; now = !now) {
             const float* k = p.coefficients + 3 * i;
-            const int now = i & 1;
-            const bool last = i + 1 == p.steps;
-            OrthoProductArgs g{};
-            g.each = l.each;
-            g.tickets = tickets;
-            g.slots = reinterpret_cast<float*>(tickets + kOrthoTickets);
-            g.bf16 = p.dtype == AR_BF16;
-            // A = X X^T
-            g.p = g.q = w + l.x[now];
-            g.c = g.ct = w + l.a;
-            g.m = g.n = l.m;
-            g.k = padded(l.n) / kPiece;
-            g.symmetric = 1;
-            g.s_acc = (float)std::ldexp(1.0, ea[i] - 2 * ex[i]);
-            e = launch_ortho_product(out, count, g, s);
+            int group = 1;
+            for (double wide = 1.0; l.merged && group < kMergeMost && i + group < p.steps; ++group) {
+                // what the group's later steps take for A is off by that much more
+                wide *= widening(k + 3 * (group - 1), tops[i + group - 1]);
+                if (!(wide <= (p.dtype == AR_BF16 ? 256.0 : 16.0)))
+                    break;
+            }
+            const int end = i + group;
+            const bool last = end == p.steps;
+            const double scale = last ? (double)p.scale : 1.0;
+            const _Float16 *x = w + l.x[now], *xt = w + l.xt[now];
+            square(x, x, nullptr, A, long_k, std::ldexp(1.0, ea[i] - 2 * ex[i]), 0.0, 0.0);
+            // the last product's factor of X: B, beside a X, or the group's polynomial F
+            uint64_t factor = l.square[1];
+            int factor_e = eb[i];
+            if (group == 1) {
+                const Factors f = factors(i);
+                square(w + A, w + A, w + A, factor, short_k, f.b_acc, f.b_add, 0.0);
+            } else {
+                uint64_t T = l.square[2], Q = factor, other = l.square[3], spare = l.square[4];
+                double f_top = 1.0;
+                for (int j = i;; ++j) {
+                    const float* kj = p.coefficients + 3 * j;
+                    // Q = a I + b A + c A A
+                    const int eq = exponent(sampled(tops[j], [&](double v) { return q_of(kj, v); }));
+                    square(w + A, w + A, w + A, Q, short_k, std::ldexp((double)kj[2], eq - 2 * ea[j]),
+                           std::ldexp((double)kj[1], eq - ea[j]), std::ldexp((double)kj[0], eq));
+                    f_top *= sampled(tops[j], [&](double v) { return q_of(kj, v); });
+                    const int ef = exponent(f_top);
+                    if (j == i) {
+                        factor_e = eq;  // F = Q
+                    } else {            // F = Q F
+                        const uint64_t to = j == i + 1 ? spare : T;
+                        square(w + Q, w + factor, nullptr, to, short_k, std::ldexp(1.0, ef - eq - factor_e),
+                               0.0, 0.0);
+                        factor = to;
+                        factor_e = ef;
+                    }
+                    if (j + 1 == end)
+                        break;
+                    // A of the next step is Q A Q, by T = Q A: they commute
+                    const int et = exponent(tops[j] * tops[j + 1]);
+                    square(w + Q, w + A, nullptr, T, short_k, std::ldexp(1.0, et - eq - ea[j]), 0.0, 0.0);
+                    square(w + Q, w + T, nullptr, A, short_k, std::ldexp(1.0, ea[j + 1] - eq - et), 0.0,
+                           0.0);
+                    std::swap(Q, other);
+                }
+            }
             if (e != hipSuccess)
                 break;
-            // B = b A + c A A
-            g.p = g.q = g.dt = w + l.a;
-            g.c = g.ct = w + l.b;
-            g.k = padded(l.m) / kPiece;
-            g.s_acc = (float)std::ldexp((double)k[2], eb[i] - 2 * ea[i]);
-            g.s_add = (float)std::ldexp((double)k[1], eb[i] - ea[i]);
-            e = launch_ortho_product(out, count, g, s);
-            if (e != hipSuccess)
-                break;
-            // X = a X + B X
-            g.p = w + l.b;
-            g.q = w + l.xt[now];
-            g.dt = w + l.xt[now];
-            g.c = w + l.x[!now];
-            g.ct = w + l.xt[!now];
-            g.n = l.n;
-            g.symmetric = 0;
-            const double up = std::ldexp(last ? (double)p.scale : 1.0, ex[i + 1] - ex[i]);
-            g.s_acc = (float)std::ldexp(up, -eb[i]);
-            g.s_add = (float)((double)k[0] * up);
-            g.last = last;
-            g.transposed = tall;
-            g.out_stride = p.out_stride;
-            e = launch_ortho_product(out, count, g, s);
+            OrthoProductArgs c = g;
+            c.p = w + factor;
+            c.q = xt;
+            c.c = w + l.x[!now];
+            c.ct = w + l.xt[!now];
+            c.m = l.m;
+            c.n = l.n;
+            c.k = short_k;
+            c.last = last;
+            if (group == 1) {  // X = a X + B X
+                const Factors f = factors(i);
+                c.dt = xt;
+                c.s_acc = f.x_acc;
+                c.s_add = f.x_add;
+            } else {  // X = F X
+                c.s_acc = (float)std::ldexp(scale, ex[end] - ex[i] - factor_e);
+            }
+            e = launch_ortho_product(out, count, c, s);
+            i = end;
         }
         if (e != hipSuccess)
             return done(e);

@@ -88,3 +88,98 @@ def next_step(y, k, coefficients):
     y = (y.t() if tall else y).to(D)
     z, dz = step(y, 2.0 ** -24 * y.abs(), ks[k], *tops(ks)[k])
     return (z.t() if tall else z), 1.001 * (dz.t() if tall else dz)
+
+
+def by_groups(rows, cols):
+    m, n = sorted((rows, cols))
+    return 10 * n >= 13 * m and m * n >= 1 << 20
+
+
+def groups_of(rows, cols, coefficients, most):
+    """The groups in which steps of a large wide or tall matrix are taken: up to three,
+    while what they make of an error of A stays below `most` times it."""
+    m, n = sorted((rows, cols))
+    steps, i, out = len(coefficients), 0, []
+    top = [t for t, _ in tops(coefficients)]
+    while i < steps:
+        group, wide = 1, 1.0
+        while by_groups(m, n) and group < 3 and i + group < steps:
+            a, b, c = coefficients[i + group - 1]
+            s = torch.linspace(0, top[i + group - 1], 257, dtype=D)
+            wide *= float(((a + b * s ** 2 + c * s ** 4) * (a + 3 * b * s ** 2 + 5 * c * s ** 4)).abs().max())
+            if wide > most:
+                break
+            group += 1
+        out.append(group)
+        i += group
+    return out
+
+
+def steps_of(X, part):
+    """X after the steps of `part`."""
+    for a, b, c in part:
+        A = X @ X.t() if X.shape[0] <= X.shape[1] else X.t() @ X
+        Q = b * A + c * A @ A
+        X = a * X + (Q @ X if X.shape[0] <= X.shape[1] else X @ Q)
+    return X
+
+
+def group_error(X, part):
+    """2-norm of all elements' errors (before the last rounding) of steps `part`
+    taken from X as one group: A = X X^T and Q = a I + b A + c A A, then for the next
+    step A = Q (Q A), its Q, and F = Q F, at last F X.
+
+    To first order each loss goes through what follows by itself.  A loss E of a
+    matrix reaches a polynomial of it as its elements (in the basis of the matrix's
+    singular vectors) times the polynomial's divided differences, so its 2-norm
+    grows by |p'|'s maximum over the singular values' range, with both signs for the
+    odd polynomial that the steps make of X; a loss of a factor grows by the other
+    factors' largest singular values."""
+    X = X.to(D)
+    X = X.t() if X.shape[0] > X.shape[1] else X
+    size = lambda t: float(t.norm())  # noqa: E731
+
+    def slopes_of(v, part):  # values and slopes of s -> s q(s^2), step by step, and of prod q by s^2
+        f, df = v.clone(), torch.ones_like(v)
+        for a, b, c in part:
+            f, df = a * f + b * f ** 3 + c * f ** 5, df * (a + 3 * b * f ** 2 + 5 * c * f ** 4)
+        return f, df
+
+    def factor_of(u, part):  # prod q as a polynomial of A, and its slope
+        g, dg, l, dl = torch.ones_like(u), torch.zeros_like(u), u.clone(), torch.ones_like(u)
+        for a, b, c in part:
+            q, dq = a + b * l + c * l * l, (b + 2 * c * l) * dl
+            g, dg = g * q, dg * q + g * dq
+            l, dl = l * q * q, dl * q * q + 2 * l * q * dq
+        return float(g.abs().max()), float(dg.abs().max())
+
+    def lost(P, Q):
+        return (2.0 ** -22 + 3 * P.shape[1] * 2.0 ** -23) * size(P.abs() @ Q.abs())
+
+    def kept(V):  # in halves, whose exponent is that of a bound up to 8 times the largest
+        return size(halved(V, 8 * float(torch.linalg.matrix_norm(V, 2)))) + 2.0 ** -23 * size(V)
+    top = float(torch.linalg.matrix_norm(X, 2))
+    out = kept(X) * float(slopes_of(torch.linspace(0, top, 4097, dtype=D), part)[1].abs().max())
+    A, F, eye = X @ X.t(), None, torch.eye(len(X), dtype=D, device=X.device)
+    dA, above = lost(X, X.t()), top  # above: |F X|
+    for j, (a, b, c) in enumerate(part):
+        u = torch.linspace(0, float(torch.linalg.matrix_norm(A, 2)), 4097, dtype=D)
+        out += (dA + kept(A)) * factor_of(u, part[j:])[1] * above
+        Q = a * eye + b * A + c * A @ A
+        dQ = abs(c) * lost(A, A) + 2.0 ** -22 * size(A) * (abs(b) + abs(c)) + kept(Q)
+        T = Q @ A
+        A2 = Q @ T
+        after = torch.linspace(0, float(torch.linalg.matrix_norm(A2, 2)), 4097, dtype=D)
+        g, dg = factor_of(after, part[j + 1:])
+        dF = dQ * above
+        if F is not None:
+            dF += (lost(Q, F) + kept(Q @ F)) * top
+        F = Q if F is None else Q @ F
+        above = float(torch.linalg.matrix_norm(F @ X, 2))
+        out += dF * g
+        if j + 1 < len(part):
+            out += dQ * 2 * float(torch.linalg.matrix_norm(T, 2)) * dg * above
+            q = float(torch.linalg.matrix_norm(Q, 2))
+            dA = q * (lost(Q, A) + kept(T)) + lost(Q, T)
+            A = A2
+    return 1.01 * (out + lost(F, X))

@@ -138,3 +138,23 @@ def test_bounds_hold_for_a_plain_computation():
         y = a * y + (b * A + c * A @ A) @ y
         assert bool(((y.double() - value).abs() <= slack).all())
     assert float(slack.norm()) < 0.003 * float(value.norm())
+
+
+def test_groups_of_steps_form():
+    """A float32 computation by groups is the same polynomial, and within the
+    bound, which a step left out is not."""
+    x = _matrix(20, 60, 5)
+    ks = [COEFFICIENTS] * 5
+    assert of.groups_of(1000, 2000, ks, 16.0) == [2, 2, 1] and of.groups_of(2000, 1000, ks, 256.0) == [3, 2]
+    assert of.groups_of(20, 60, ks, 256.0) == of.groups_of(2000, 2500, ks, 256.0) == [1] * 5
+    for group, tight in ((1, 2.0 ** -12), (2, 2.0 ** -10), (3, 2.0 ** -5)):
+        before = x / (x.norm() + 1e-7)
+        value, y = of.steps_of(before, ks[:group]), before.float()
+        A, F = y @ y.t(), None
+        for a, b, c in ks[:group]:
+            Q = a * torch.eye(20) + b * A + c * A @ A
+            F = Q if F is None else Q @ F
+            A = Q @ (Q @ A)
+        bound = of.group_error(before, ks[:group])
+        assert float(((F @ y).double() - value).norm()) <= bound < tight * float(value.norm())
+    assert torch.allclose(of.steps_of(x.t() / (x.norm() + 1e-7), ks).t(), of.orthogonalize(x, 5, ks, 1e-7))

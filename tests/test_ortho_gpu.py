@@ -52,23 +52,43 @@ def _one_step(env, m, n, dtype="f32", coefficients=COEFFICIENTS, scale=1.0, pad=
 
 
 def _steps(env, m, n, steps=5, coefficients=COEFFICIENTS, x=None, seed=0):
-    """Each step's float32 result against a step from the one before; bfloat16
-    is the same with one more rounding."""
+    """Steps one by one: each one's float32 result against a step from the one
+    before, and bfloat16 is the same with one more rounding.  Steps by groups: the
+    2-norm of all errors of each group after the one before, and of bfloat16's first."""
     torch, api, dev = env["torch"], env["api"], env["dev"]
     x = _host(env, (m, n), seed, "bf16", 0.02).float() if x is None else x
     ks = of.coefficient_list(coefficients, steps)
-    before = None
-    for k in range(steps):
+
+    def call(x, k):
         y = torch.empty_like(x, device=dev)
-        api.orthogonalize(x.to(dev), y, k + 1, ks[:k + 1], EPS)
+        api.orthogonalize(x.to(dev), y, k, ks[:k], EPS)
         torch.cuda.synchronize()
-        value, slack = of.next_step(before, k, ks) if k else of.one_step(x, ks[0], EPS)
-        ob.between(y, value, slack, (m, n, k))
-        before = y.cpu()
-    b = torch.empty_like(x, dtype=torch.bfloat16, device=dev)
-    api.orthogonalize(x.to(dev).bfloat16(), b, steps, ks, EPS)
-    if torch.equal(x.bfloat16().float(), x):
-        assert torch.equal(b, y.bfloat16()), (m, n)
+        return y.cpu()
+    if not of.by_groups(m, n):
+        before = None
+        for k in range(steps):
+            y = call(x, k + 1)
+            value, slack = of.next_step(before, k, ks) if k else of.one_step(x, ks[0], EPS)
+            ob.between(y, value, slack, (m, n, k))
+            before = y
+        if torch.equal(x.bfloat16().float(), x):
+            assert torch.equal(call(x.bfloat16(), steps), y.bfloat16()), (m, n)
+        return
+    before, i = of.start(x, EPS), 0
+    for group in of.groups_of(m, n, ks, 16.0):
+        y = call(x, i + group)
+        value = of.steps_of(before, ks[i:i + group])
+        error, bound = float((y.double() - value).norm()), of.group_error(before, ks[i:i + group])
+        print(m, n, "steps", i, "to", i + group, "error", error, "bound", bound, "of", float(value.norm()))
+        assert error <= bound
+        before, i = y.double(), i + group
+    z = x.bfloat16()
+    first = of.groups_of(m, n, ks, 256.0)[0]
+    before = of.start(z, EPS)
+    value = of.steps_of(before, ks[:first])
+    error = float((call(z, first).double() - value).norm())
+    bound = of.group_error(before, ks[:first])
+    assert error <= bound + 2.0 ** -8 * (float(value.norm()) + bound)
 
 
 SIDES = [(1, 1), (1, 7), (2, 2), (5, 3), (31, 33), (32, 32), (33, 64), (64, 128), (65, 40), (100, 260),
@@ -107,6 +127,48 @@ def test_larger(env, m, n):
     _one_step(env, m, n, "f32")
     _one_step(env, m, n, "bf16")
     _steps(env, m, n)
+
+
+@pytest.mark.parametrize("m,n", [(900, 1200), (1500, 1000)])
+def test_steps_by_groups(env, m, n):
+    """Also three at once, whose sums are split otherwise."""
+    torch, api, dev = env["torch"], env["api"], env["dev"]
+    _steps(env, m, n)
+    x = _host(env, (3, m, n), 8)
+    y = torch.empty_like(x, device=dev)
+    api.orthogonalize(x.to(dev), y, 2, COEFFICIENTS, EPS)
+    torch.cuda.synchronize()
+    for i in range(3):
+        before = of.start(x[i], EPS)
+        value = of.steps_of(before, [COEFFICIENTS] * 2)
+        assert float((y[i].cpu().double() - value).norm()) <= of.group_error(before, [COEFFICIENTS] * 2)
+
+
+@pytest.mark.parametrize("m,n", [(900, 1170), (1170, 900), (64, 16390), (10500, 100), (201, 5301), (1001, 2500)])
+@pytest.mark.parametrize("steps", (2, 3, 5, 7))
+def test_groups_of_steps(env, m, n, steps):
+    """Steps by groups, on a matrix with one element in each row and column (of the
+    shorter side): each element goes by the polynomials alone, and an element of a
+    product has one term, so that nothing but halves' and float32's roundings is
+    lost: three steps widen an error 2^-20 of A by up to 141, and what is off by
+    more than 2^-12 is in the wrong place, or is not that polynomial."""
+    torch, api, dev = env["torch"], env["api"], env["dev"]
+    g = torch.Generator().manual_seed(m + n + steps)
+    k = min(m, n)
+    x = torch.zeros(m, n)
+    at = torch.randperm(m, generator=g)[:k], torch.randperm(n, generator=g)[:k]
+    x[at] = torch.exp(torch.rand(k, generator=g) * 4 - 2) * torch.sign(torch.rand(k, generator=g) - 0.5)
+    x = x.bfloat16().float()
+    y, b = torch.empty(m, n, device=dev), torch.empty(m, n, device=dev, dtype=torch.bfloat16)
+    api.orthogonalize(x.to(dev), y, steps, COEFFICIENTS, EPS)
+    api.orthogonalize(x.to(dev).bfloat16(), b, steps, COEFFICIENTS, EPS)
+    s = x.double() / (x.double().norm() + EPS)
+    for _ in range(steps):
+        s = 3.4445 * s - 4.7750 * s ** 3 + 2.0315 * s ** 5
+    torch.cuda.synchronize()
+    assert bool(((y.cpu().double() - s).abs() <= 2.0 ** -12).all())
+    assert bool(((b.cpu().double() - s).abs() <= 2.0 ** -12 + 2.0 ** -8 * s.abs()).all())
+    assert bool((y.cpu()[x == 0] == 0).all()) and bool((b.cpu()[x == 0] == 0).all())
 
 
 @pytest.mark.parametrize("count,m,n,steps", [(1, 100, 2500, 2), (1, 2300, 70, 2), (1, 2900, 2900, 1),
