@@ -614,28 +614,33 @@ def orthogonalize(x, y, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e
     (a, b, c), or three for each step.  Without ``workspace``
     (``orthogonalize_workspace``) one is allocated; a smaller one, down to that
     of one matrix, takes the matrices in parts."""
-    xs, ys = _matrices(x), _matrices(y)
-    if not xs and not ys:
+    (xs, count, first), (ys, count_y, _) = _matrices(x), _matrices(y)
+    if not count and not count_y:
         return y
+    if count != count_y:
+        raise ValueError("x are %d matrices, y %d" % (count, count_y))
     flat = [float(c) for row in coefficients for c in (row if hasattr(row, "__len__") else (row,))]
     if len(flat) == 3:
         flat = flat * steps
     if len(flat) != 3 * steps:
         raise ValueError("coefficients must be three, or three for each of %d steps" % steps)
     if workspace is None:
-        workspace = _own_workspace(stream, orthogonalize_workspace, len(xs), xs[0].shape[0],
-                                   xs[0].shape[-1], xs[0].dtype, xs[0].device)
+        workspace = _own_workspace(stream, orthogonalize_workspace, count, first.shape[-2],
+                                   first.shape[-1], first.dtype, first.device)
     rc = (_bound and _bound[0] or binding()).orthogonalize(xs, ys, flat, eps, scale, workspace,
-                                                           _stream_of(xs[0], stream))
+                                                           _stream_of(first, stream))
     if rc:
         raise ArError(rc, "ar_orthogonalize")
     return y
 
 
 def _matrices(x):
+    """What the binding takes, how many matrices, and a tensor of their sizes."""
     if isinstance(x, (list, tuple)):
-        return list(x)
-    return [x] if x.dim() == 2 else list(x.unbind(0))
+        return list(x), len(x), x[0] if len(x) else None
+    if x.dim() not in (2, 3):
+        raise ValueError("matrices must have shape ([count,] rows, cols), got %s" % (tuple(x.shape),))
+    return x, 1 if x.dim() == 2 else x.shape[0], x
 
 
 class TensorList:

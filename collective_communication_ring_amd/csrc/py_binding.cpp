@@ -546,45 +546,74 @@ PyObject* head_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// How many matrices a list of them, or a tensor [count, rows, cols] or [rows, cols], holds.
+Py_ssize_t matrix_count(PyObject* o, const char* what)
+{
+    if (PyList_Check(o))
+        return PyList_GET_SIZE(o);
+    const at::Tensor& t = tensor(o, what);
+    return t.dim() == 3 ? (Py_ssize_t)t.size(0) : 1;
+}
+
+// Their addresses, and the distance of their rows.
+template <class P>
+void matrices_of(PyObject* o, int64_t device, const int64_t (&shape)[2], at::ScalarType type,
+                 const char* what, std::vector<P>* at, size_t* stride)
+{
+    if (!PyList_Check(o)) {
+        const at::Tensor& t = tensor(o, what);
+        if (t.dim() != 3) {
+            (*at)[0] = rows_of(t, device, shape, type, what, stride);
+            return;
+        }
+        const int64_t all[] = {(int64_t)at->size(), shape[0], shape[1]};
+        check(t, device, all, type, what);
+        if (t.stride(2) != 1 && shape[1] > 1)
+            throw Refused(std::string("the last dimension of ") + what + " must be contiguous");
+        *stride = (size_t)t.stride(1);
+        for (size_t i = 0; i < at->size(); ++i)
+            (*at)[i] = static_cast<char*>(t.data_ptr()) + i * (size_t)t.stride(0) * t.element_size();
+        return;
+    }
+    for (size_t i = 0; i < at->size(); ++i) {
+        size_t own = 0;
+        (*at)[i] = rows_of(tensor(PyList_GET_ITEM(o, (Py_ssize_t)i), what), device, shape, type, what, &own);
+        if (i && shape[0] > 1 && own != *stride)
+            throw Refused(std::string("the rows of all of ") + what + " must be equally far apart");
+        *stride = own;
+    }
+}
+
 // orthogonalize(x, y, coefficients, eps, scale, workspace, stream) -> status; x and y are lists of
-// matrices, or one of [count, rows, cols] each; coefficients a list of 3 numbers for each step
+// matrices, or tensors [count, rows, cols] or [rows, cols]; coefficients a list of 3 numbers for
+// each step
 PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
         expect(n, 7);
-        if (!PyList_Check(a[0]) || !PyList_Check(a[1]) || !PyList_Check(a[2]))
+        if (!PyList_Check(a[2]))
             throw Refused("wrong arguments");
-        const Py_ssize_t count = PyList_GET_SIZE(a[0]);
-        if (!count || PyList_GET_SIZE(a[1]) != count)
+        const Py_ssize_t count = matrix_count(a[0], "x");
+        if (!count || matrix_count(a[1], "y") != count)
             throw Refused("x and y must be as many matrices, one at least");
         ar_orthogonalize_t p = {};
-        const at::Tensor &x0 = tensor(PyList_GET_ITEM(a[0], 0), "x"),
-                         &y0 = tensor(PyList_GET_ITEM(a[1], 0), "y"), &workspace = tensor(a[5], "workspace");
+        const at::Tensor &x0 = tensor(PyList_Check(a[0]) ? PyList_GET_ITEM(a[0], 0) : a[0], "x"),
+                         &workspace = tensor(a[5], "workspace");
         const at::ScalarType type = x0.scalar_type();
         p.dtype = code_of(type);
         if (p.dtype != AR_FLOAT32 && p.dtype != AR_BF16)
             throw Refused("x has dtype " + type_text(type) + ": float32 or bfloat16 is wanted");
         if (!x0.is_cuda())
             throw Refused("x must be on the GPU");
-        if (x0.dim() != 2 || y0.dim() != 2)
-            throw Refused("a matrix must have shape (rows, cols), got " +
-                          shape_text(x0.dim() != 2 ? x0.sizes() : y0.sizes()));
-        const int64_t dev = x0.get_device(), rows = x0.size(0), cols = x0.size(1);
+        const int64_t d = x0.dim();
+        if (d != 2 && (d != 3 || PyList_Check(a[0])))
+            throw Refused("a matrix must have shape (rows, cols), got " + shape_text(x0.sizes()));
+        const int64_t dev = x0.get_device(), rows = x0.size(d - 2), cols = x0.size(d - 1);
         const int64_t shape[] = {rows, cols};
         std::vector<const void*> x((size_t)count);
         std::vector<void*> y((size_t)count);
-        const auto matrix = [&](PyObject* o, const char* what, size_t* stride, Py_ssize_t i) {
-            size_t own = 0;
-            void* at = rows_of(tensor(o, what), dev, shape, type, what, &own);
-            if (i && rows > 1 && own != *stride)
-                throw Refused(std::string("the rows of all of ") + what + " must be equally far apart");
-            *stride = own;
-            return at;
-        };
-        for (Py_ssize_t i = 0; i < count; ++i) {
-            x[(size_t)i] = matrix(PyList_GET_ITEM(a[0], i), "x", &p.x_stride, i);
-            y[(size_t)i] = matrix(PyList_GET_ITEM(a[1], i), "y", &p.out_stride, i);
-        }
+        matrices_of(a[0], dev, shape, type, "x", &x, &p.x_stride);
+        matrices_of(a[1], dev, shape, type, "y", &y, &p.out_stride);
         const Py_ssize_t numbers = PyList_GET_SIZE(a[2]);
         if (numbers % 3)
             throw Refused("each step has three coefficients");

@@ -662,6 +662,10 @@ size_t ar_head_rmsnorm_backward_workspace(int ranks, size_t dim); /* 0 for sizes
  * Every product is held to about float32's accuracy: X, A and b A + c A A are
  * kept as two 16-bit floats each (22 significant bits), and their products are
  * three matrix products of those with float32 sums; the norm's sum is 64-bit.
+ * Steps of a large matrix much longer one way than the other may be taken up to
+ * three together, X multiplied once by the product of their polynomials in A.
+ * The order of sums depends on sizes, the number of matrices and the workspace's
+ * size alone.
  * A matrix of zeros gives zeros (eps > 0); one with an infinity or NaN gives
  * NaN.
  * x and out are HOST arrays of device addresses, read during the call only;

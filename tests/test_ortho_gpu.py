@@ -92,7 +92,8 @@ def _steps(env, m, n, steps=5, coefficients=COEFFICIENTS, x=None, seed=0):
 
 
 SIDES = [(1, 1), (1, 7), (2, 2), (5, 3), (31, 33), (32, 32), (33, 64), (64, 128), (65, 40), (100, 260),
-         (127, 129), (128, 128), (129, 300), (257, 255), (300, 40), (8, 700), (700, 3)]
+         (127, 129), (128, 128), (129, 300), (257, 255), (300, 40), (8, 700), (700, 3),
+         (32, 512), (480, 20), (64, 256), (65, 128), (96, 128), (97, 128), (127, 90)]  # about LDS's room
 
 
 @pytest.mark.parametrize("m,n", SIDES)
@@ -220,6 +221,21 @@ def test_special_values(env):
             assert bool(torch.isnan(y).all())
 
 
+@pytest.mark.parametrize("m,n", [(130, 300), (1200, 900)])
+def test_special_values_of_larger(env, m, n):
+    torch, api, dev = env["torch"], env["api"], env["dev"]
+    for dt in env["types"].values():
+        x = torch.zeros(m, n, dtype=dt, device=dev)
+        y = torch.full_like(x, 3.0)
+        api.orthogonalize(x, y)
+        assert bool((y == 0).all())
+        for bad in (float("inf"), float("nan")):
+            x = torch.randn(m, n, device=dev).to(dt)
+            x[77, 101] = bad
+            api.orthogonalize(x, y)
+            assert bool(torch.isnan(y).all())
+
+
 def _same(env, got, want):
     assert all(env["torch"].equal(a, b) for a, b in zip(got, want))
 
@@ -276,11 +292,53 @@ def test_repeats_and_graph(env):
         assert torch.equal(y, z), k
 
 
+@pytest.mark.parametrize("shape", [(3, 40, 50), (2, 1150, 920)])
+def test_forms_of_the_arguments(env, shape):
+    """Matrices that lie in turn in rows of one array, one of them by itself, a
+    list for a tensor, on another stream, in place, and from a graph replayed
+    between eager calls: the same bits."""
+    torch, api, dev = env["torch"], env["api"], env["dev"]
+    count, m, n = shape
+    x = _host(env, shape, 9).to(dev)
+    want = torch.empty_like(x)
+    api.orthogonalize(x, want)
+    room = torch.full((m, count, n + 5), 7.0, device=dev)
+    turn = room.permute(1, 0, 2)[:, :, :n]
+    turn.copy_(x)
+    y = torch.empty_like(x)
+    api.orthogonalize(turn, list(y))
+    assert torch.equal(y, want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    api.orthogonalize(list(turn), turn, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(turn, want) and bool((room[:, :, n:] == 7.0).all())
+    ws, z = api.orthogonalize_workspace(*shape), torch.empty_like(x)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        api.orthogonalize(x, z, workspace=ws)
+    for k in range(4):
+        if k == 2:
+            x.add_(0.01)
+        z.zero_()
+        g.replay()
+        api.orthogonalize(x, y)
+        torch.cuda.synchronize()
+        assert torch.equal(y, z), k
+    assert api.orthogonalize([], []) == []
+    assert api.orthogonalize(x[:0], y[:0]).shape[0] == 0
+
+
 def test_wrapper_refuses(env):
     torch, api, dev = env["torch"], env["api"], env["dev"]
     x, y = (torch.zeros(2, 30, 40, device=dev) for _ in range(2))
     ws = api.orthogonalize_workspace(2, 30, 40)
     for call in (lambda: api.orthogonalize(x, y[:1], workspace=ws),
+                 lambda: api.orthogonalize(x, []), lambda: api.orthogonalize([], y),
+                 lambda: api.orthogonalize(x[None], y[None]), lambda: api.orthogonalize(x[0, 0], y[0, 0]),
+                 lambda: api.orthogonalize([x], [y], workspace=ws),
+                 lambda: api.orthogonalize(x, list(y)[:1], workspace=ws),
+                 lambda: api.orthogonalize(x, y[:, :, :20], workspace=ws),
                  lambda: api.orthogonalize(x, y.bfloat16(), workspace=ws),
                  lambda: api.orthogonalize(x, y.cpu(), workspace=ws),
                  lambda: api.orthogonalize(x.double(), y.double(), workspace=ws),
