@@ -661,7 +661,10 @@ __device__ inline void small_load(const _Float16* s, uint32_t r, uint32_t c, uin
 
 // All steps of a matrix by one workgroup, 16 waves, a block of a product each: what
 // a product makes stays in registers until all waves have read what it replaces.
-// 160 x 96, five steps: 41 us, and 91 by a launch a product.
+// 160 x 96, five steps: 41 us, and 91 by a launch a product; 40 of them 43.  Bound by
+// the way from one product to the next: a step of one block is 2.1 us, of 160 x 96's
+// fifteen 6.6, 3 of them matrix instructions (the loads of LDS one round ahead: 42
+// us; only A's and B's lower triangle: 40, but 64 x 64 23 for 21).
 template <class E>
 __global__ __launch_bounds__(kSmallThreads) void k_ortho_small(OrthoPointers in, OrthoPointers out,
                                                                OrthoSmallArgs a)
@@ -849,8 +852,9 @@ namespace {
 
 // What a tile's side costs, in microseconds: a piece of the tiles of one round
 // of workgroups (`slots` of them are resident), when they are few and when the
-// chip is full of them, and what a launch takes besides (the first copies and
-// the tile's way out).  Measured at 64 x 64 to 4096 x 8192.  The wide tiles read
+// chip is full of them, and what a round takes besides (the first copies and
+// the tile's way out; counted once a launch, twelve 1024 x 1024, five steps: 1.20
+// ms, by rounds 1.16).  Measured at 64 x 64 to 4096 x 8192.  The wide tiles read
 // LDS and the L2s less for a product and fill the chip's matrix cores (256 x 256:
 // 4096 x 8192 with K = 4096 in 641 us, 1.29 PFLOP/s, what the library's float16
 // product reaches; 128 x 128: 718), the small ones are spread over more of it
@@ -875,7 +879,9 @@ double time_of(const Form& f, const OrthoProductArgs& a, int count)
     double piece = (double)(tiles / f.slots) * f.full;
     if (rest)
         piece += f.few + (f.full - f.few) * (double)rest / f.slots;
-    return piece * a.k + f.besides;
+    // a round's beginnings and ends, of which two workgroups of a CU hide half
+    const double rounds = (double)((tiles + f.slots - 1) / f.slots);
+    return piece * a.k + f.besides * (f.slots > 256 ? (rounds + 1.0) / 2.0 : rounds);
 }
 
 template <int B, int WM, int WN, int S, bool PARTS>

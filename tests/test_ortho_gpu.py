@@ -173,7 +173,8 @@ def test_groups_of_steps(env, m, n, steps):
 
 
 @pytest.mark.parametrize("count,m,n,steps", [(1, 100, 2500, 2), (1, 2300, 70, 2), (1, 2900, 2900, 1),
-                                             (1, 4096, 4100, 1), (1, 4400, 4096, 1), (9, 1030, 1000, 2)])
+                                             (1, 4096, 4100, 1), (1, 4400, 4096, 1), (9, 1030, 1000, 2),
+                                             (1, 2048, 2048, 2), (1, 4096, 4096, 1)])
 def test_every_tile(env, count, m, n, steps):
     """Sizes at which each tile is taken for each product (64 to 256 wide, whole
     and by parts), against the form computed on the GPU; with two steps, the
