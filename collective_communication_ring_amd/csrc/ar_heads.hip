@@ -139,7 +139,8 @@ hipError_t launch_heads(int dtype, bool norm, HeadsArgs a, hipStream_t s)
     a.stream = (uint64_t)a.rows * a.dim * (dtype == AR_BF16 ? 2 : 4) > kStreamBytes;
     const uint32_t group = 64 / a.lanes, waves = kThreads / 64;
     const auto table = [&](uint32_t turns) {  // cosines and sines of a wave's tokens
-        return ((group * turns + a.heads.by - 2) / a.heads.by + 1) * a.turn.pairs;
+        const uint32_t n = group * turns;  // whole tokens, or it may begin within one
+        return (n % a.heads.by ? (n + a.heads.by - 2) / a.heads.by + 1 : n / a.heads.by) * a.turn.pairs;
     };
     // Rounds of a wave: those of whole tokens, 4 at least, where enough waves are left
     // to fill the chip (8 ranks' 2048 x 10 heads of 128: 19.9 us by 4 or 5 rounds, 22.1
@@ -152,7 +153,7 @@ hipError_t launch_heads(int dtype, bool norm, HeadsArgs a, hipStream_t s)
     a.turns = whole < 4 ? (3 + whole) / whole * whole : whole;
     if (a.turns > 8 || rounds / a.turns < 4096)
         a.turns = std::max(1u, std::min(4u, rounds / 4096));
-    while (a.turns > 1 && table(a.turns) > 512)
+    while (a.turns > 1 && table(a.turns) > 1024)
         --a.turns;
     a.table = table(a.turns);
     const size_t lds = waves * a.table * sizeof(float2) + (norm ? 8 * (size_t)a.dim : 0);
