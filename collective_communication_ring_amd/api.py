@@ -421,8 +421,10 @@ def binding():
         raise RuntimeError("_binding.so is not built (in %s); run __graft_entry__.build()" % HERE)
     from . import _binding
     _binding.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-                    (L.ar_rmsnorm, L.ar_reduce_scatter_rmsnorm, L.ar_rmsnorm_backward, L.ar_rotary,
-                     L.ar_head_rmsnorm, L.ar_head_rmsnorm_backward, L.ar_orthogonalize)))
+                    (L.ar_rmsnorm, L.ar_reduce_scatter_rmsnorm, L.ar_rmsnorm_backward)))
+    _binding.init_heads(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                          (L.ar_rotary, L.ar_head_rmsnorm, L.ar_head_rmsnorm_backward,
+                           L.ar_orthogonalize)))
     _bound = (_binding, L)
     return _binding
 

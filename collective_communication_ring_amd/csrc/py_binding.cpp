@@ -3,7 +3,7 @@
 //
 // A norm of one row takes 3 us on the GPU; reading five properties of each of
 // six tensors took the wrapper as long in Python.  The C entry points are
-// called by the addresses that init() is given, so they are those of the
+// called by the addresses that init() and init_heads() are given, so they are those of the
 // library that the package has loaded.  Nothing is kept from call to call.
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -207,28 +207,37 @@ PyObject* status_of(F entry, Args... args)
     return PyLong_FromLong(rc);
 }
 
-void expect(Py_ssize_t got, Py_ssize_t want)
+void expect(Py_ssize_t got, Py_ssize_t want, bool given = p_rmsnorm)
 {
     if (got != want)
         throw Refused("wrong number of arguments");
-    if (!p_rmsnorm)
+    if (!given)
         throw Refused("the binding has not been given the library's entry points");
 }
 
-// init(ar_rmsnorm, ar_reduce_scatter_rmsnorm, ar_rmsnorm_backward, ar_rotary, ar_head_rmsnorm,
-// ar_head_rmsnorm_backward, ar_orthogonalize): addresses.
+// init(ar_rmsnorm, ar_reduce_scatter_rmsnorm, ar_rmsnorm_backward): addresses.
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
-        if (n != 7)
+        if (n != 3)
             throw Refused("wrong number of arguments");
-        p_rotary = reinterpret_cast<decltype(p_rotary)>(handle(a[3]));
-        p_head_rmsnorm = reinterpret_cast<decltype(p_head_rmsnorm)>(handle(a[4]));
-        p_head_rmsnorm_backward = reinterpret_cast<decltype(p_head_rmsnorm_backward)>(handle(a[5]));
-        p_orthogonalize = reinterpret_cast<decltype(p_orthogonalize)>(handle(a[6]));
         p_rmsnorm = reinterpret_cast<decltype(p_rmsnorm)>(handle(a[0]));
         p_reduce_scatter_rmsnorm = reinterpret_cast<decltype(p_reduce_scatter_rmsnorm)>(handle(a[1]));
         p_rmsnorm_backward = reinterpret_cast<decltype(p_rmsnorm_backward)>(handle(a[2]));
+        Py_RETURN_NONE;
+    });
+}
+
+// init_heads(ar_rotary, ar_head_rmsnorm, ar_head_rmsnorm_backward, ar_orthogonalize): addresses.
+PyObject* init_heads(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        if (n != 4)
+            throw Refused("wrong number of arguments");
+        p_rotary = reinterpret_cast<decltype(p_rotary)>(handle(a[0]));
+        p_head_rmsnorm = reinterpret_cast<decltype(p_head_rmsnorm)>(handle(a[1]));
+        p_head_rmsnorm_backward = reinterpret_cast<decltype(p_head_rmsnorm_backward)>(handle(a[2]));
+        p_orthogonalize = reinterpret_cast<decltype(p_orthogonalize)>(handle(a[3]));
         Py_RETURN_NONE;
     });
 }
@@ -456,7 +465,7 @@ bool all_or_none(PyObject* const* a, std::initializer_list<int> which, const cha
 PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
-        expect(n, 10);
+        expect(n, 10, p_rotary);
         ar_rotary_t p = {};
         const at::Tensor& q = tensor(a[0], "q");
         const HeadShape s = head_shape(q, &p.dtype);
@@ -480,7 +489,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n)
 PyObject* head_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
-        expect(n, 12);
+        expect(n, 12, p_head_rmsnorm);
         ar_head_rmsnorm_t p = {};
         const at::Tensor& q = tensor(a[0], "q");
         const HeadShape s = head_shape(q, &p.dtype);
@@ -507,7 +516,7 @@ PyObject* head_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n)
 PyObject* head_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
-        expect(n, 17);
+        expect(n, 17, p_head_rmsnorm_backward);
         ar_head_rmsnorm_backward_t p = {};
         const at::Tensor &q = tensor(a[1], "q"), &q_dweight = tensor(a[4], "q_dweight"),
                          &workspace = tensor(a[15], "workspace");
@@ -590,7 +599,7 @@ void matrices_of(PyObject* o, int64_t device, const int64_t (&shape)[2], at::Sca
 PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
-        expect(n, 7);
+        expect(n, 7, p_orthogonalize);
         if (!PyList_Check(a[2]))
             throw Refused("wrong arguments");
         const Py_ssize_t count = matrix_count(a[0], "x");
@@ -702,7 +711,7 @@ PyObject* is_dense(PyObject*, PyObject* const* a, Py_ssize_t n)
 }
 
 #define METHOD(f) {#f, (PyCFunction)(void*)f, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(init), METHOD(rmsnorm), METHOD(reduce_scatter_rmsnorm),
+PyMethodDef methods[] = {METHOD(init), METHOD(init_heads), METHOD(rmsnorm), METHOD(reduce_scatter_rmsnorm),
                          METHOD(rmsnorm_backward), METHOD(rotary), METHOD(head_rmsnorm),
                          METHOD(head_rmsnorm_backward), METHOD(orthogonalize), METHOD(spans),
                          METHOD(same_layout),
