@@ -3,8 +3,8 @@
 //
 // A norm of one row takes 3 us on the GPU; reading five properties of each of
 // six tensors took the wrapper as long in Python.  The C entry points are
-// called by the addresses that init() and init_heads() are given, so they are those of the
-// library that the package has loaded.  Nothing is kept from call to call.
+// called by the addresses that init() and init_heads() are given, so they are
+// those of the library that the package has loaded.  Nothing is kept from call to call.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
