@@ -12,10 +12,18 @@
 namespace ar {
 
 // A matrix in halves: value = (hi + lo) 2^-e, hi the nearest float16 of value
-// 2^e and lo that of what is left, 22 significant bits of the two.  The host
-// keeps e such that no value of the matrix passes 2^14; below it the bits of a
-// value end at 2^-24, 2^-38 of the largest, so a matrix's error stays near
-// 2^-23 of its norm however its values spread.
+// 2^e and lo that of what is left: 22 significant bits of the two, off by 2^-23 of
+// the value.  e is such that no value passes 2^14, by a bound of the matrix's
+// singular values; the bits of a value end at 2^-24, so one below 2^-14 of the
+// bound has fewer: it is off by 2^-39 of the bound.  Against the whole matrix's norm
+// that is little; a row or column that is that much smaller than the others loses
+// it for itself.
+//
+// The bound has two parts.  The host finds what X can reach, step by step, from a
+// norm of 1.  A matrix whose norm is below eps starts further down, X in
+// (2^-(t + 1), 2^-t], and t is found on the device: its arrays are kept 2^d
+// higher, with d = max(0, t - h), h the powers of two by which the steps before can
+// have brought X closer to the host's bound (OrthoLift).
 //
 // It is kept in pieces of 32 columns, piece by piece: 128 bytes a row, 32 hi and
 // then 32 lo, all rows of a piece behind one another, so that what a tile's
@@ -28,11 +36,21 @@ constexpr uint32_t padded(uint32_t n) { return (n + kPiece - 1) / kPiece * kPiec
 constexpr int kOrthoTop = 14;
 
 constexpr int kOrthoBatch = 128;  // matrices of one round of launches, at most
-constexpr int kNormParts = 512;   // partial sums of a matrix's norm, at most
+constexpr int kNormParts = 512;   // partial sums of a matrix's norm, at most; its t lies behind them
 
 struct OrthoPointers {
     const void* p[kOrthoBatch];
 };
+
+// How far above the host's exponents a product's factors are for a matrix that
+// starts 2^-t down: with n = max(0, t - now), m = max(0, t - next) and b = max(0, 2 n - b)
+// the sums' factor gets 2^(acc . (n, m, b)), the addend's 2^(add . (n, m, b)).
+struct OrthoLift {
+    int now, next, b;
+    int acc[3], add[3];
+};
+constexpr int kOrthoGround = 1 << 20;  // a `next` of the result: 0 whatever t
+constexpr int kOrthoMostLift = 400;    // t at most: 2^-278 is the smallest float beside the largest eps
 
 struct OrthoSplitArgs {
     double* parts;        // [count][kNormParts], of which nparts are in use (set by the launch)
@@ -59,6 +77,8 @@ struct OrthoProductArgs {
     int symmetric;              // C is (m == n, c == ct): tiles of the lower triangle only, each
                                 //   written to both its places
     float s_acc, s_add, diag;
+    OrthoLift lift;
+    const int* down;            // t of the first matrix, each / 2 ahead of the next one's
     // the last product: C goes to the caller's arrays instead, [m][n] or transposed
     int last, transposed, bf16;
     uint64_t out_stride;
@@ -100,7 +120,10 @@ struct OrthoSmallArgs {
     struct {
         float a, b_acc, b_add, x_acc, x_add;
     } step[kOrthoMaxSteps];
+    short lift[kOrthoMaxSteps + 1];    // OrthoLift's now; the last: kOrthoSmallGround
+    short lift_b[kOrthoMaxSteps];      // its b
 };
+constexpr int kOrthoSmallGround = 30000;
 
 hipError_t launch_ortho_small(const OrthoPointers& x, const OrthoPointers& out, int count,
                               const OrthoSmallArgs& a, hipStream_t s);

@@ -51,6 +51,18 @@ __global__ __launch_bounds__(kThreads) void k_ortho_norm(OrthoPointers x, OrthoS
         a.parts[blockIdx.y * (a.each / 4) + blockIdx.x] = sum;
 }
 
+// t of a matrix whose X has this norm (OrthoLift): 0 for one near 1, and for zeros
+// and what is no number.
+__device__ inline int down_of(double norm)
+{
+    if (!(norm > 0.0 && norm < 0.5))
+        return 0;
+    const int t = -__builtin_amdgcn_frexp_exp(norm);
+    return t < kOrthoMostLift ? t : kOrthoMostLift;
+}
+
+__device__ inline int above(int v) { return v > 0 ? v : 0; }
+
 __device__ inline void split(float v, _Float16* hi, _Float16* lo)
 {
     *hi = (_Float16)v;
@@ -92,9 +104,14 @@ __global__ __launch_bounds__(kThreads) void k_ortho_split(OrthoPointers x, Ortho
         double sum = 0.0;
         for (uint32_t i = threadIdx.x; i < a.nparts; i += 64)
             sum += a.parts[blockIdx.z * (a.each / 4) + i];
-        sum = wave_sum(sum);
-        if (threadIdx.x == 0)
-            s_up = a.up / (sqrt(sum) + (double)a.eps);
+        const double norm = sqrt(wave_sum(sum));
+        if (threadIdx.x == 0) {
+            const double by = norm + (double)a.eps;
+            const int down = down_of(norm / by);
+            s_up = ldexp(a.up, down) / by;
+            if (blockIdx.x == 0 && blockIdx.y == 0)
+                *reinterpret_cast<int*>(a.parts + blockIdx.z * (a.each / 4) + kNormParts) = down;
+        }
     }
     const uint32_t r0 = blockIdx.y * kTile, c0 = blockIdx.x * kTile;
     float v[2][8];
@@ -422,7 +439,8 @@ __global__ __launch_bounds__(64 * (B / WM) * (B / WN)) void k_ortho_product(Orth
     // in registers by now: a load of them on its way would have the loop wait for
     // all of its reads of LDS
     void* to = const_cast<void*>(out.p[matrix]);
-    __asm__ __volatile__("" ::"s"(to), "s"(a.out_stride));
+    const int down = a.down[matrix * (a.each / 2)];
+    __asm__ __volatile__("" ::"s"(to), "s"(a.out_stride), "s"(down));
     const uint32_t lds = lds_address(s_piece);
 #pragma unroll
     for (uint32_t o = 0; o < S; ++o) {
@@ -519,6 +537,13 @@ __global__ __launch_bounds__(64 * (B / WM) * (B / WN)) void k_ortho_product(Orth
     // product: four consecutive values of a row of C^T, and, after four lanes
     // exchanged theirs, of a row of C
     const uint32_t mp = padded(a.m), np = padded(a.n);
+    float s_acc = a.s_acc, s_add = a.s_add;
+    if (down) {
+        const OrthoLift& l = a.lift;
+        const int now = above(down - l.now), next = above(down - l.next), b = above(2 * now - l.b);
+        s_acc = ldexpf(s_acc, l.acc[0] * now + l.acc[1] * next + l.acc[2] * b);
+        s_add = ldexpf(s_add, l.add[0] * now + l.add[1] * next + l.add[2] * b);
+    }
     const _Float16* dt = a.dt ? a.dt + own : nullptr;
     _Float16 *c = a.c + own, *ct = a.ct + own;
     each_of<TM * TN>([&](auto number) {
@@ -539,9 +564,9 @@ __global__ __launch_bounds__(64 * (B / WM) * (B / WN)) void k_ortho_product(Orth
                 float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    v[r] = g.acc[x][y][4 * r4 + r] * a.s_acc;
+                    v[r] = g.acc[x][y][4 * r4 + r] * s_acc;
                     if (dt)
-                        v[r] = fmaf((float)dh[r] + (float)dl[r], a.s_add, v[r]);
+                        v[r] = fmaf((float)dh[r] + (float)dl[r], s_add, v[r]);
                     v[r] += i + r == j ? a.diag : 0.0f;
                     v[r] = i + r < a.m && j < a.n ? v[r] : 0.0f;
                 }
@@ -698,7 +723,9 @@ __global__ __launch_bounds__(kSmallThreads) void k_ortho_small(OrthoPointers in,
         for (int z = 0; z < 4; ++z)
             sum = fma((double)v[g.value][z], (double)v[g.value][z], sum);
     });
-    const double up = a.up / (sqrt(block_sum<kSmallWaves>(sum, s_f)) + (double)a.eps);
+    const double norm = sqrt(block_sum<kSmallWaves>(sum, s_f)), by = norm + (double)a.eps;
+    const int down = __builtin_amdgcn_readfirstlane(down_of(norm / by));
+    const double up = ldexp(a.up, down) / by;
     each_of<kHeld>([&](auto g) {
         const uint32_t i = g.value * kSmallThreads + threadIdx.x;
         const uint32_t r = i / cp * 4, c = i % cp / 4 * 4;
@@ -732,7 +759,15 @@ __global__ __launch_bounds__(kSmallThreads) void k_ortho_small(OrthoPointers in,
         });
     };
     for (int step = 0;; ++step) {
-        const auto k = a.step[step];
+        auto k = a.step[step];
+        if (down) {  // as OrthoLift of the products
+            const int now = above(down - a.lift[step]), next = above(down - a.lift[step + 1]);
+            const int b = above(2 * now - a.lift_b[step]);
+            k.b_acc = ldexpf(k.b_acc, b - 4 * now);
+            k.b_add = ldexpf(k.b_add, b - 2 * now);
+            k.x_acc = ldexpf(k.x_acc, next - now - b);
+            k.x_add = ldexpf(k.x_add, next - now);
+        }
         if (has_a) {  // A = X X^T; A is its own transpose
             acc = small_tile(x, mp, ai, x, mp, aj, np, lane);
             values(ai, aj, [&](auto g, uint32_t i, uint32_t j) {

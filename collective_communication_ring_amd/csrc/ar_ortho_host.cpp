@@ -45,7 +45,7 @@ Layout layout_of(size_t rows, size_t cols)
     l.n = (uint32_t)std::max(rows, cols);
     const uint64_t x = whole((uint64_t)l.m * 2 * padded(l.n)), xt = whole((uint64_t)l.n * 2 * padded(l.m)),
                    a = whole((uint64_t)l.m * 2 * padded(l.m));
-    uint64_t at = whole(kNormParts * sizeof(double) / 2);  // the norm's parts come first
+    uint64_t at = whole((kNormParts + 1) * sizeof(double) / 2);  // the norm's parts come first
     for (uint64_t* p : {&l.x[0], &l.x[1]}) {
         *p = at;
         at += x;
@@ -91,6 +91,16 @@ double largest(const float* k, double top, bool whole_step)
     return most;
 }
 
+// Largest |a + b s^2 + c s^4| for s of [0, top].
+double steepest(const float* k, double top)
+{
+    const double a = k[0], b = k[1], c = k[2], t = top * top;
+    double most = std::max(std::fabs(a), std::fabs(a + t * (b + t * c)));
+    if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < t)
+        most = std::max(most, std::fabs(a - b * b / (4.0 * c)));
+    return most;
+}
+
 // Largest |f(s)| for s of [0, top], of polynomials of low degree: by samples, that
 // miss less than a hundredth of it (an exponent has room for three times).
 template <class F>
@@ -112,11 +122,13 @@ double widening(const float* k, double top)
     });
 }
 
-// The exponent that leaves values up to `most` at 2^kOrthoTop.
-int exponent(double most)
+// The power of two that values up to `most` stay below, and the exponent that
+// leaves it at 2^kOrthoTop.
+int power(double most)
 {
-    return kOrthoTop - (most > 0.0 ? std::max(-100, std::ilogb(most) + 1) : -100);
+    return most > 0.0 ? std::min(2000, std::max(-100, std::ilogb(most) + 1)) : -100;
 }
+int exponent(double most) { return kOrthoTop - power(most); }
 
 // Bytes ahead of the matrices' arrays: the tickets and, where a side is long
 // enough for products to go by parts, their slots.
@@ -177,12 +189,14 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             return AR_ERR_INVALID_ARG;
 
     // how large X and b A + c A A get, step by step, and their exponents
-    std::vector<int> ex, eb, ea;
+    std::vector<int> ex, eb, ea, down, down_b;  // down, down_b: OrthoLift's now and b
     std::vector<double> tops;  // of X's singular values
     try {
         ex.resize(p.steps + 1);
         ea.resize(p.steps);
         eb.resize(p.steps);
+        down.resize(p.steps + 1);
+        down_b.resize(p.steps);
         tops.resize(p.steps + 1);
         const size_t z = size_of(p.dtype);
         const uint64_t len = p.cols * z, step_x = p.x_stride * z, step_out = p.out_stride * z;
@@ -219,16 +233,24 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
     } catch (...) {
         return AR_ERR_INTERNAL;
     }
-    double top = tops[0] = 1.0;
+    double top = tops[0] = 1.0, grown = 1.0;  // grown: at most, of an X that is small throughout
     for (int i = 0; i < p.steps; ++i) {
+        const float* k = p.coefficients + 3 * i;
+        const double b_top = largest(k, top, false);
         ex[i] = exponent(top);
         ea[i] = exponent(top * top);
-        eb[i] = exponent(largest(p.coefficients + 3 * i, top, false));
-        top = tops[i + 1] = largest(p.coefficients + 3 * i, top, true);
+        eb[i] = exponent(b_top);
+        down[i] = std::max(0, power(grown) - power(top));
+        // of b A + c A A, against A
+        const double slope = std::max(std::fabs((double)k[1]), std::fabs(k[1] + top * top * k[2]));
+        down_b[i] = std::max(0, 2 * power(top) + power(slope) - power(b_top));
+        grown *= steepest(k, top);
+        top = tops[i + 1] = largest(k, top, true);
         if (!(top <= 65536.0))
             return AR_ERR_UNSUPPORTED;
     }
     ex[p.steps] = 0;
+    down[p.steps] = kOrthoGround;
 
     // what a step's sums and addends are multiplied by: coefficients, exponents, and
     // in the end the scale
@@ -267,7 +289,10 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             for (int i = 0; i < p.steps; ++i) {
                 const Factors f = factors(i);
                 a.step[i] = {f.a, f.b_acc, f.b_add, f.x_acc, f.x_add};
+                a.lift[i] = (short)std::min(down[i], kOrthoSmallGround);
+                a.lift_b[i] = (short)std::min(down_b[i], kOrthoSmallGround);
             }
+            a.lift[p.steps] = kOrthoSmallGround;
             const hipError_t e = launch_ortho_small(in, out, count, a, s);
             if (e != hipSuccess)
                 return done(e);
@@ -289,13 +314,15 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
         OrthoProductArgs g{};
         g.each = l.each;
         g.tickets = tickets;
+        g.down = reinterpret_cast<const int*>(split.parts + kNormParts);
         g.slots = reinterpret_cast<float*>(tickets + kOrthoTickets);
         g.bf16 = p.dtype == AR_BF16;
         g.transposed = tall;
         g.out_stride = p.out_stride;
         // A symmetric product of square arrays: to = acc p q (+ add d + diag I)
         const auto square = [&](const _Float16* x, const _Float16* y, const _Float16* d, uint64_t to,
-                                uint32_t pieces, double acc, double add, double diag) {
+                                uint32_t pieces, double acc, double add, double diag,
+                                const OrthoLift& lift) {
             if (e != hipSuccess)
                 return;
             OrthoProductArgs c = g;
@@ -309,6 +336,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             c.s_acc = (float)acc;
             c.s_add = (float)add;
             c.diag = (float)diag;
+            c.lift = lift;
             e = launch_ortho_product(out, count, c, s);
         };
         const uint32_t long_k = padded(l.n) / kPiece, short_k = padded(l.m) / kPiece;
@@ -327,13 +355,14 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             const bool last = end == p.steps;
             const double scale = last ? (double)p.scale : 1.0;
             const _Float16 *x = w + l.x[now], *xt = w + l.xt[now];
-            square(x, x, nullptr, A, long_k, std::ldexp(1.0, ea[i] - 2 * ex[i]), 0.0, 0.0);
+            square(x, x, nullptr, A, long_k, std::ldexp(1.0, ea[i] - 2 * ex[i]), 0.0, 0.0, {});
             // the last product's factor of X: B, beside a X, or the group's polynomial F
             uint64_t factor = l.square[1];
             int factor_e = eb[i];
             if (group == 1) {
                 const Factors f = factors(i);
-                square(w + A, w + A, w + A, factor, short_k, f.b_acc, f.b_add, 0.0);
+                square(w + A, w + A, w + A, factor, short_k, f.b_acc, f.b_add, 0.0,
+                       {down[i], 0, down_b[i], {-4, 0, 1}, {-2, 0, 1}});
             } else {
                 uint64_t T = l.square[2], Q = factor, other = l.square[3], spare = l.square[4];
                 double f_top = 1.0;
@@ -342,7 +371,8 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
                     // Q = a I + b A + c A A
                     const int eq = exponent(sampled(tops[j], [&](double v) { return q_of(kj, v); }));
                     square(w + A, w + A, w + A, Q, short_k, std::ldexp((double)kj[2], eq - 2 * ea[j]),
-                           std::ldexp((double)kj[1], eq - ea[j]), std::ldexp((double)kj[0], eq));
+                           std::ldexp((double)kj[1], eq - ea[j]), std::ldexp((double)kj[0], eq),
+                           {down[j], 0, 0, {-4, 0, 0}, {-2, 0, 0}});
                     f_top *= sampled(tops[j], [&](double v) { return q_of(kj, v); });
                     const int ef = exponent(f_top);
                     if (j == i) {
@@ -350,7 +380,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
                     } else {            // F = Q F
                         const uint64_t to = j == i + 1 ? spare : T;
                         square(w + Q, w + factor, nullptr, to, short_k, std::ldexp(1.0, ef - eq - factor_e),
-                               0.0, 0.0);
+                               0.0, 0.0, {});
                         factor = to;
                         factor_e = ef;
                     }
@@ -358,9 +388,11 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
                         break;
                     // A of the next step is Q A Q, by T = Q A: they commute
                     const int et = exponent(tops[j] * tops[j + 1]);
-                    square(w + Q, w + A, nullptr, T, short_k, std::ldexp(1.0, et - eq - ea[j]), 0.0, 0.0);
+                    const OrthoLift lift = {down[j], down[j + 1], 0, {-1, 1, 0}, {}};
+                    square(w + Q, w + A, nullptr, T, short_k, std::ldexp(1.0, et - eq - ea[j]), 0.0, 0.0,
+                           lift);
                     square(w + Q, w + T, nullptr, A, short_k, std::ldexp(1.0, ea[j + 1] - eq - et), 0.0,
-                           0.0);
+                           0.0, lift);
                     std::swap(Q, other);
                 }
             }
@@ -380,8 +412,10 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
                 c.dt = xt;
                 c.s_acc = f.x_acc;
                 c.s_add = f.x_add;
+                c.lift = {down[i], down[end], down_b[i], {-1, 1, -1}, {-1, 1, 0}};
             } else {  // X = F X
                 c.s_acc = (float)std::ldexp(scale, ex[end] - ex[i] - factor_e);
+                c.lift = {down[i], down[end], 0, {-1, 1, 0}, {}};
             }
             e = launch_ortho_product(out, count, c, s);
             i = end;

@@ -660,7 +660,8 @@ size_t ar_head_rmsnorm_backward_workspace(int ranks, size_t dim); /* 0 for sizes
  *       A = X X^T,  X = a X + (b A + c A A) X     (rows > cols: X^T X, from the right)
  *   out = scale * X
  * Every product is held to about float32's accuracy: X, A and b A + c A A are
- * kept as two 16-bit floats each (22 significant bits), and their products are
+ * kept as two 16-bit floats each (22 significant bits), under powers of two of
+ * each matrix's own, whatever its norm is beside eps, and their products are
  * three matrix products of those with float32 sums; the norm's sum is 64-bit.
  * Steps of a large matrix much longer one way than the other may be taken up to
  * three together, X multiplied once by the product of their polynomials in A.
