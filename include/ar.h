@@ -659,12 +659,18 @@ size_t ar_head_rmsnorm_backward_workspace(int ranks, size_t dim); /* 0 for sizes
  *   `steps` times, with (a, b, c) = coefficients[step]:
  *       A = X X^T,  X = a X + (b A + c A A) X     (rows > cols: X^T X, from the right)
  *   out = scale * X
- * Every product is held to about float32's accuracy: X, A and b A + c A A are
- * kept as two 16-bit floats each (22 significant bits), under powers of two of
+ * X, A and b A + c A A are kept as two 16-bit floats each, under powers of two of
  * each matrix's own, whatever its norm is beside eps, and their products are
  * three matrix products of those with float32 sums; the norm's sum is 64-bit.
+ * So an element is off by 2^-23 of itself, or by 2^-37 of X's norm (later, of
+ * what the steps can have made of it) where that is more.  Against the whole
+ * matrix it is float32's accuracy; a row or column far smaller than the others
+ * is known less exactly by itself than float32 products would know it (rows of
+ * 512 that are 1e-5 of the others: 6e-5 of their own size, 1e-6: 6e-4).
  * Steps of a large matrix much longer one way than the other may be taken up to
- * three together, X multiplied once by the product of their polynomials in A.
+ * three together, X multiplied once by the product of their polynomials in A,
+ * while that widens A's roundings by at most 16 (bfloat16, which rounds the
+ * result to 2^-9: 256, a part of 2^-15).
  * The order of sums depends on sizes, the number of matrices and the workspace's
  * size alone.
  * A matrix of zeros gives zeros (eps > 0); one with an infinity or NaN gives
