@@ -2,6 +2,9 @@
 // checks, the workspace's layout, and the sequence of products.
 #include <algorithm>
 #include <cmath>
+#include <deque>
+#include <map>
+#include <utility>
 #include <vector>
 
 #include "ar_checks.h"
@@ -138,16 +141,48 @@ size_t shared_bytes(const Layout& l)
            (padded(l.n) >= kOrthoPartPieces * 2 * kPiece ? kOrthoSlots * kOrthoSlotBytes : 0);
 }
 
-// Whether two matrices share a byte; rows of one stride may lie in turn.
-bool meet(uintptr_t x, uintptr_t y, uint64_t rows, uint64_t len, uint64_t step_x, uint64_t step_y)
-{
-    if (x + (rows - 1) * step_x + len <= y || y + (rows - 1) * step_y + len <= x)
-        return false;
-    if (step_x != step_y || rows == 1)
-        return true;
-    const uint64_t d = y >= x ? (y - x) % step_x : (step_x - (x - y) % step_x) % step_x;
-    return d < len || d + len > step_x;
-}
+// Matrices of one kind (inputs or outputs) that reach past the address a walk over
+// all of them has come to, by where their rows begin modulo the rows' distance.
+// (Rows that lie in turn in one array: every matrix reaches past every other one,
+// and is next to two of them there.)
+class Reaching {
+public:
+    Reaching(uint64_t reach, uint64_t step) : reach_(reach), step_(step) {}
+    void add(uintptr_t at, size_t i)
+    {
+        order_.push_back({at, by_.insert({at % step_, {at, i}})});
+    }
+    // leaves out what ends at `at` or ahead of it
+    void walk_to(uintptr_t at)
+    {
+        for (; !order_.empty() && order_.front().first + reach_ <= at; order_.pop_front())
+            by_.erase(order_.front().second);
+    }
+    // whether any but matrix `i` at this address shares a byte with rows of `len`
+    // bytes, `step` apart; rows of another distance are taken to
+    bool meets(uintptr_t at, uint64_t len, uint64_t step, size_t i) const
+    {
+        if (by_.empty())
+            return false;
+        if (step != step_)
+            return true;
+        const auto other = [&](uint64_t from, uint64_t to) {  // beginning in [from, to)
+            for (auto v = by_.lower_bound(from); v != by_.end() && v->first < to; ++v)
+                if (v->second.first != at || v->second.second != i)
+                    return true;
+            return false;
+        };
+        const uint64_t r = at % step, low = r + 1, high = r + len;  // r - len < beginning < r + len
+        return other(low > len ? low - len : 0, std::min(high, step)) ||
+               (low < len && other(step + low - len, step)) || (high > step && other(0, high - step));
+    }
+
+private:
+    typedef std::multimap<uint64_t, std::pair<uintptr_t, size_t>> By;
+    uint64_t reach_, step_;
+    By by_;
+    std::deque<std::pair<uintptr_t, By::iterator>> order_;
+};
 
 }  // namespace
 
@@ -200,7 +235,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
         tops.resize(p.steps + 1);
         const size_t z = size_of(p.dtype);
         const uint64_t len = p.cols * z, step_x = p.x_stride * z, step_out = p.out_stride * z;
-        // out against everything, in order of address
+        // out against everything, in order of address; out[i] may be x[i]
         struct Item {
             uintptr_t at;
             size_t i;
@@ -215,20 +250,17 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
         std::sort(items.begin(), items.end(), [](const Item& x, const Item& y) { return x.at < y.at; });
         const uint64_t reach_x = (p.rows - 1) * step_x + len, reach_out = (p.rows - 1) * step_out + len;
         const uintptr_t ws = (uintptr_t)p.workspace, ws_end = ws + shared + room * l.each * 2;
-        for (size_t i = 0; i < items.size(); ++i) {
-            const Item& v = items[i];
-            const uint64_t reach = v.out ? reach_out : reach_x;
-            if (v.at < ws_end && ws < v.at + reach)
+        Reaching ins(reach_x, step_x), outs(reach_out, step_out);
+        for (const Item& v : items) {
+            if (v.at < ws_end && ws < v.at + (v.out ? reach_out : reach_x))
                 return AR_ERR_INVALID_USAGE;
-            for (size_t j = i + 1; j < items.size() && items[j].at < v.at + reach; ++j) {
-                const Item& w = items[j];
-                if (!v.out && !w.out)
-                    continue;
-                const bool own = v.i == w.i && v.out != w.out && v.at == w.at && step_x == step_out;
-                if (!own && meet(v.at, w.at, p.rows, len, v.out ? step_out : step_x,
-                                 w.out ? step_out : step_x))
-                    return AR_ERR_INVALID_USAGE;
-            }
+            ins.walk_to(v.at);
+            outs.walk_to(v.at);
+            const uint64_t step = v.out ? step_out : step_x;
+            if (outs.meets(v.at, len, step, v.out ? SIZE_MAX : v.i) ||
+                (v.out && ins.meets(v.at, len, step, v.i)))
+                return AR_ERR_INVALID_USAGE;
+            (v.out ? outs : ins).add(v.at, v.i);
         }
     } catch (...) {
         return AR_ERR_INTERNAL;
