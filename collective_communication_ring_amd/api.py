@@ -605,6 +605,18 @@ def orthogonalize_workspace(count, rows, cols, dtype=None, device="cuda"):
                        device=device)
 
 
+# The most that orthogonalize takes for a workspace of its own, in bytes, where one
+# matrix needs no more: some 90 million elements at once fill the GPU many times over.
+_ORTHOGONALIZE_OWN = 2 << 30
+
+
+def _orthogonalize_room(count, rows, cols):
+    """How many matrices that workspace holds."""
+    one = ar_orthogonalize_workspace(1, rows, cols)
+    each = ar_orthogonalize_workspace(2, rows, cols) - one
+    return min(count, 1 + max(0, _ORTHOGONALIZE_OWN - one) // each) if each else count
+
+
 def orthogonalize(x, y, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7, scale=1.0,
                   workspace=None, stream=None):
     """Orthogonalises matrices of one shape by Newton-Schulz steps
@@ -614,8 +626,8 @@ def orthogonalize(x, y, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e
     x, y: float32 or bfloat16, [rows, cols], [count, rows, cols], or a list of
     [rows, cols] (rows equally far apart in all); y may be x.  coefficients:
     (a, b, c), or three for each step.  Without ``workspace``
-    (``orthogonalize_workspace``) one is allocated; a smaller one, down to that
-    of one matrix, takes the matrices in parts."""
+    (``orthogonalize_workspace``) one is allocated, of 2 GiB or one matrix's; a
+    smaller one, down to that of one matrix, takes the matrices in parts."""
     (xs, count, first), (ys, count_y, _) = _matrices(x), _matrices(y)
     if not count and not count_y:
         return y
@@ -627,8 +639,9 @@ def orthogonalize(x, y, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e
     if len(flat) != 3 * steps:
         raise ValueError("coefficients must be three, or three for each of %d steps" % steps)
     if workspace is None:
-        workspace = _own_workspace(stream, orthogonalize_workspace, count, first.shape[-2],
-                                   first.shape[-1], first.dtype, first.device)
+        sizes = first.shape[-2], first.shape[-1]
+        workspace = _own_workspace(stream, orthogonalize_workspace, _orthogonalize_room(count, *sizes),
+                                   *sizes, first.dtype, first.device)
     rc = (_bound and _bound[0] or binding()).orthogonalize(xs, ys, flat, eps, scale, workspace,
                                                            _stream_of(first, stream))
     if rc:
