@@ -612,6 +612,9 @@ _ORTHOGONALIZE_OWN = 2 << 30
 
 def _orthogonalize_room(count, rows, cols):
     """How many matrices that workspace holds."""
+    m, n = (-(-side // 32) * 32 for side in sorted((rows, cols)))
+    if m * n <= 16384 and 4 * m * (2 * n + m) <= 163584:
+        return min(count, 1)  # they stay in LDS
     one = ar_orthogonalize_workspace(1, rows, cols)
     each = ar_orthogonalize_workspace(2, rows, cols) - one
     return min(count, 1 + max(0, _ORTHOGONALIZE_OWN - one) // each) if each else count

@@ -217,8 +217,10 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
     const size_t shared = shared_bytes(l);
     if (!p.workspace || p.workspace_bytes < shared + l.each * 2 || (uintptr_t)p.workspace % 256)
         return AR_ERR_INVALID_ARG;
-    const size_t room = std::min<size_t>(
-        std::min<size_t>((p.workspace_bytes - shared) / (l.each * 2), p.count), kOrthoBatch);
+    // (matrices that stay in LDS leave the workspace alone)
+    const bool small = ortho_small(l.m, l.n);
+    const size_t held = small ? kOrthoBatch : (p.workspace_bytes - shared) / (l.each * 2);
+    const size_t room = std::min<size_t>(std::min<size_t>(held, p.count), kOrthoBatch);
     for (size_t i = 0; i < p.count; ++i)
         if (!p.x[i] || !p.out[i] || misaligned(p.x[i], p.dtype) || misaligned(p.out[i], p.dtype))
             return AR_ERR_INVALID_ARG;
@@ -249,7 +251,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
         }
         std::sort(items.begin(), items.end(), [](const Item& x, const Item& y) { return x.at < y.at; });
         const uint64_t reach_x = (p.rows - 1) * step_x + len, reach_out = (p.rows - 1) * step_out + len;
-        const uintptr_t ws = (uintptr_t)p.workspace, ws_end = ws + shared + room * l.each * 2;
+        const uintptr_t ws = (uintptr_t)p.workspace, ws_end = ws + shared + (small ? 1 : room) * l.each * 2;
         Reaching ins(reach_x, step_x), outs(reach_out, step_out);
         for (const Item& v : items) {
             if (v.at < ws_end && ws < v.at + (v.out ? reach_out : reach_x))
@@ -308,7 +310,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             in.p[i] = p.x[first + i];
             out.p[i] = p.out[first + i];
         }
-        if (ortho_small(l.m, l.n)) {
+        if (small) {
             OrthoSmallArgs a{};
             a.x_stride = p.x_stride;
             a.out_stride = p.out_stride;

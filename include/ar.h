@@ -685,7 +685,8 @@ size_t ar_head_rmsnorm_backward_workspace(int ranks, size_t dim); /* 0 for sizes
  * successful no-op.  `workspace` is ar_orthogonalize_workspace bytes of device
  * memory, 256-byte aligned, whose contents mean nothing between calls; a
  * smaller one of at least the bytes for one matrix is used for one part of
- * the matrices after another. */
+ * the matrices after another.  (Matrices of up to 16384 elements, both sides
+ * rounded up to 32, that LDS holds are not put there: one matrix's serves all.) */
 typedef struct {
     int dtype; /* AR_FLOAT32 or AR_BF16: x, out */
     int steps;
