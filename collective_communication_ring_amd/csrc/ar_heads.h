@@ -104,6 +104,24 @@ constexpr int kHeadPerLane = 16;  // elements of a head that a thread holds
 constexpr int kHeadBackBlocks = 768;
 inline int head_back_blocks(int ranks) { return kHeadBackBlocks / ranks; }
 
+// LDS of the backward pass, in bytes: both weights at 0, from `sums` on the sums of
+// the side that a wave is not at (read 16 bytes at a time), from `angles` on the
+// waves' angles; at the end, from 0 on, a partial row of each wave.
+struct HeadBackPlaces {
+    uint32_t sums, angles, bytes;
+};
+inline __host__ __device__ HeadBackPlaces head_back_places(uint32_t dim, uint32_t threads, uint32_t waves,
+                                                           uint32_t wave_angles)
+{
+    HeadBackPlaces p;
+    p.sums = (dim + 1) / 2 * 16;
+    p.angles = p.sums + threads * kHeadPerLane * 4;
+    p.bytes = p.angles + waves * wave_angles * 8;
+    const uint32_t rows = waves * dim * 4;
+    p.bytes = p.bytes < rows ? rows : p.bytes;
+    return p;
+}
+
 // Elements of a vector: the widest of 16 bytes and less that divides a head,
 // and in the layout of halves the half that is rotated.
 int heads_vector(int dtype, uint32_t dim, const Turn& t);

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kThreads, (back_waves<E, W>())) void k_heads_back(H
 {
     using H = Head<E, W, LAYOUT, WHOLE>;
     using T = typename E::T;
-    extern __shared__ float2 s_table[];
+    extern __shared__ float4 s_all[];
     const uint32_t group = 64 / a.lanes, sub = (threadIdx.x & 63u) / a.lanes;
     const uint32_t lane = (threadIdx.x & 63u) - sub * a.lanes;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -45,9 +45,11 @@ __global__ __launch_bounds__(kThreads, (back_waves<E, W>())) void k_heads_back(H
     int one = a.heads[0] ? 0 : 1, two = a.heads[1] ? 1 : 0;  // first and last side there is
     // LDS: both weights (in registers they cost a wave on each SIMD), the waves' sums
     // of the side they are not at, their angles
-    float* s_w = reinterpret_cast<float*>(s_table);
-    float4* s_acc = reinterpret_cast<float4*>(s_table + a.dim) + threadIdx.x;
-    float2* table = s_table + a.dim + kThreads * kHeadPerLane / 2 + wave * (a.chunk * a.turn.pairs);
+    const HeadBackPlaces places = head_back_places(a.dim, kThreads, kThreads / 64, a.chunk * a.turn.pairs);
+    float* s_w = reinterpret_cast<float*>(s_all);
+    float4* s_acc = s_all + places.sums / 16 + threadIdx.x;
+    float2* table = reinterpret_cast<float2*>(s_all) + places.angles / 8 +
+                    wave * (a.chunk * a.turn.pairs);
     float acc[kHeadPerLane];
 #pragma unroll
     for (int i = 0; i < kHeadPerLane; ++i)
@@ -192,7 +194,7 @@ __global__ __launch_bounds__(kThreads, (back_waves<E, W>())) void k_heads_back(H
     } while (++chunk < end);
 
     // the workgroup's sums: of the heads of a wave, then of the four waves
-    float* s_dw = reinterpret_cast<float*>(s_table);
+    float* s_dw = reinterpret_cast<float*>(s_all);
     float* p = a.partial + ((uint64_t)blockIdx.y * a.blocks + blockIdx.x) * 2 * a.dim;
     if (apart && one == 1)
         change_sides();
@@ -311,8 +313,7 @@ hipError_t launch_heads_back(int dtype, HeadsBackArgs a, hipStream_t s)
         const uint32_t units = a.apart ? 2 * chunks : chunks;
         a.run = (units + most * waves - 1) / (most * waves);
         a.blocks = (units + a.run * waves - 1) / (a.run * waves);
-        const size_t lds = sizeof(float2) * std::max<size_t>(
-            waves * a.dim / 2, a.dim + kThreads * kHeadPerLane / 2 + waves * a.chunk * a.turn.pairs);
+        const size_t lds = head_back_places(a.dim, kThreads, waves, a.chunk * a.turn.pairs).bytes;
         if (dtype == AR_FLOAT32)
             launch_typed<Elem<AR_FLOAT32>>(w, a, lds, s);
         else

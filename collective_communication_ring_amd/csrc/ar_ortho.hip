@@ -401,7 +401,7 @@ __global__ __launch_bounds__(64 * (B / WM) * (B / WN)) void k_ortho_product(Orth
 {
     using P = Product<B, WM, WN>;
     constexpr int TM = P::TM, TN = P::TN, THREADS = 64 * P::WAVES;
-    __shared__ _Float16 s_piece[S * P::STAGE];
+    __shared__ __attribute__((aligned(16))) _Float16 s_piece[S * P::STAGE];
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     uint32_t tile = xcd_block(blockIdx.x, gridDim.x), part = 0;
@@ -694,7 +694,7 @@ template <class E>
 __global__ __launch_bounds__(kSmallThreads) void k_ortho_small(OrthoPointers in, OrthoPointers out,
                                                                OrthoSmallArgs a)
 {
-    __shared__ _Float16 s_all[kOrthoSmallBytes / 2];
+    __shared__ __attribute__((aligned(16))) _Float16 s_all[kOrthoSmallBytes / 2];
     __shared__ double s_f[kSmallWaves];
     const typename E::T* p = static_cast<const typename E::T*>(in.p[blockIdx.x]);
     void* to = const_cast<void*>(out.p[blockIdx.x]);
