@@ -5,6 +5,7 @@
 // six tensors took the wrapper as long in Python.  The C entry points are
 // called by the addresses that init() and init_heads() are given, so they are
 // those of the library that the package has loaded.  Nothing is kept from call to call.
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -195,12 +196,15 @@ PyObject* guarded(Call call)
     return nullptr;
 }
 
-// An entry point's status.  Other Python threads run meanwhile: a launch may
-// have to wait for room in its stream's queue.
+// An entry point's status.  The tensors' GPU is the current one during the call: a
+// default stream's handle is 0 on every GPU and stands for the current one's.  Other
+// Python threads run meanwhile: a launch may have to wait for room in its stream's
+// queue.
 template <class F, class... Args>
-PyObject* status_of(F entry, Args... args)
+PyObject* status_of(int64_t device, F entry, Args... args)
 {
     int rc = 0;
+    const c10::DeviceGuard on(c10::Device(c10::DeviceType::CUDA, (c10::DeviceIndex)device));
     Py_BEGIN_ALLOW_THREADS
     rc = entry(args...);
     Py_END_ALLOW_THREADS
@@ -276,7 +280,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n)
             p.scale = static_cast<float*>(block_of(*scale, dev, scales, at::kFloat, "scale"));
         if (rstd)
             p.rstd = static_cast<float*>(block_of(*rstd, dev, {rows}, at::kFloat, "rstd"));
-        return status_of(p_rmsnorm, &p, handle(a[9]));
+        return status_of(dev, p_rmsnorm, &p, handle(a[9]));
     });
 }
 
@@ -321,7 +325,7 @@ PyObject* reduce_scatter_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n)
             p.scale = static_cast<float*>(block_of(*scale, dev, scales, at::kFloat, "scale"));
         if (rstd)
             p.rstd = static_cast<float*>(block_of(*rstd, dev, per, at::kFloat, "rstd"));
-        return status_of(p_reduce_scatter_rmsnorm, static_cast<ar_comm_t>(handle(a[0])), from, &p,
+        return status_of(dev, p_reduce_scatter_rmsnorm, static_cast<ar_comm_t>(handle(a[0])), from, &p,
                          handle(a[10]));
     });
 }
@@ -362,7 +366,7 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
         p.dweight = static_cast<float*>(block_of(dweight, dev, wshape, at::kFloat, "dweight"));
         p.workspace = workspace.data_ptr();
         p.workspace_bytes = (size_t)workspace.nbytes();
-        return status_of(p_rmsnorm_backward, &p, handle(a[8]));
+        return status_of(dev, p_rmsnorm_backward, &p, handle(a[8]));
     });
 }
 
@@ -480,7 +484,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n)
         }
         rotation_of(a + 4, s, &p.rotation);
         p.inverse = (int)integer(a[8]);
-        return status_of(p_rotary, &p, handle(a[9]));
+        return status_of(s.device, p_rotary, &p, handle(a[9]));
     });
 }
 
@@ -507,7 +511,7 @@ PyObject* head_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n)
             heads_of(tensor(a[6], "k_out"), s, (int64_t)p.k_heads, "k_out", &p.k_out);
         }
         rotation_of(a + 7, s, &p.rotation);
-        return status_of(p_head_rmsnorm, &p, handle(a[11]));
+        return status_of(s.device, p_head_rmsnorm, &p, handle(a[11]));
     });
 }
 
@@ -551,7 +555,7 @@ PyObject* head_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
             throw Refused("workspace must be a contiguous tensor on cuda:" + std::to_string(s.device));
         p.workspace = workspace.data_ptr();
         p.workspace_bytes = (size_t)workspace.nbytes();
-        return status_of(p_head_rmsnorm_backward, &p, handle(a[16]));
+        return status_of(s.device, p_head_rmsnorm_backward, &p, handle(a[16]));
     });
 }
 
@@ -642,7 +646,7 @@ PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n)
         p.coefficients = coefficients.data();
         p.workspace = workspace.data_ptr();
         p.workspace_bytes = (size_t)workspace.nbytes();
-        return status_of(p_orthogonalize, &p, handle(a[6]));
+        return status_of(dev, p_orthogonalize, &p, handle(a[6]));
     });
 }
 
