@@ -50,6 +50,7 @@ struct HeadsArgs {
     const void* weight[2];  // the norm only
     uint32_t heads0;        // of the queries
     uint32_t rows;          // batch * tokens * heads
+    uint32_t first;         // workgroup of the launch (set by it)
     FastDiv heads, tokens;  // of a token (both sides); of a batch
     uint32_t dim, nvec;     // elements and vectors of a head
     uint32_t turned;        // rotated units of a head, halves
@@ -97,6 +98,7 @@ struct HeadsBackArgs {
 };
 
 constexpr uint32_t kHeadMaxDim = 1024;
+constexpr uint32_t kHeadsMostBlocks = 1u << 23;  // of a launch: a grid has less than 2^32 threads
 constexpr int kHeadPerLane = 16;  // elements of a head that a thread holds
 
 // Workgroups of the backward pass, at most: three on each CU, as its registers

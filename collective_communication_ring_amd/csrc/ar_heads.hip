@@ -29,7 +29,7 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadsArgs a)
     const uint32_t group = 64 / a.lanes, sub = (threadIdx.x & 63u) / a.lanes;
     const uint32_t lane = (threadIdx.x & 63u) - sub * a.lanes;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const uint32_t row0 = (blockIdx.x * (kThreads / 64) + wave) * (group * a.turns);
+    const uint32_t row0 = ((a.first + blockIdx.x) * (kThreads / 64) + wave) * (group * a.turns);
     const uint32_t rows = row0 >= a.rows ? 0 : a.rows - row0 < group * a.turns ? a.rows - row0
                                                                               : group * a.turns;
     struct At {
@@ -160,13 +160,17 @@ hipError_t launch_heads(int dtype, bool norm, HeadsArgs a, hipStream_t s)
         --a.turns;
     a.table = table(a.turns);
     const size_t lds = waves * a.table * sizeof(float2) + (norm ? 8 * (size_t)a.dim : 0);
-    const uint32_t grid = (rounds + a.turns * waves - 1) / (a.turns * waves);
-    if (dtype == AR_FLOAT32)
-        norm ? launch_typed<Elem<AR_FLOAT32>, true>(w, a, lds, grid, s)
-             : launch_typed<Elem<AR_FLOAT32>, false>(w, a, lds, grid, s);
-    else
-        norm ? launch_typed<Elem<AR_BF16>, true>(w, a, lds, grid, s)
-             : launch_typed<Elem<AR_BF16>, false>(w, a, lds, grid, s);
+    const uint32_t blocks = (rounds + a.turns * waves - 1) / (a.turns * waves);
+    a.first = 0;
+    for (; a.first < blocks; a.first += kHeadsMostBlocks) {
+        const uint32_t grid = std::min(blocks - a.first, kHeadsMostBlocks);
+        if (dtype == AR_FLOAT32)
+            norm ? launch_typed<Elem<AR_FLOAT32>, true>(w, a, lds, grid, s)
+                 : launch_typed<Elem<AR_FLOAT32>, false>(w, a, lds, grid, s);
+        else
+            norm ? launch_typed<Elem<AR_BF16>, true>(w, a, lds, grid, s)
+                 : launch_typed<Elem<AR_BF16>, false>(w, a, lds, grid, s);
+    }
     return hipGetLastError();
 }
 
