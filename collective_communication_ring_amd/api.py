@@ -636,7 +636,8 @@ def orthogonalize(x, y, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e
         return y
     if count != count_y:
         raise ValueError("x are %d matrices, y %d" % (count, count_y))
-    flat = [float(c) for row in coefficients for c in (row if hasattr(row, "__len__") else (row,))]
+    rows = [k.tolist() if hasattr(k, "tolist") else k for k in coefficients]  # also of a tensor or array
+    flat = [float(c) for row in rows for c in (row if hasattr(row, "__len__") else (row,))]
     if len(flat) == 3:
         flat = flat * steps
     if len(flat) != 3 * steps:
@@ -655,6 +656,9 @@ def orthogonalize(x, y, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e
 def _matrices(x):
     """What the binding takes, how many matrices, and a tensor of their sizes."""
     if isinstance(x, (list, tuple)):
+        for t in x[:1]:
+            if t.dim() != 2:
+                raise ValueError("a matrix must have shape (rows, cols), got %s" % (tuple(t.shape),))
         return list(x), len(x), x[0] if len(x) else None
     if x.dim() not in (2, 3):
         raise ValueError("matrices must have shape ([count,] rows, cols), got %s" % (tuple(x.shape),))
