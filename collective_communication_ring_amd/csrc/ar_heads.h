@@ -101,8 +101,10 @@ constexpr uint32_t kHeadMaxDim = 1024;
 constexpr uint32_t kHeadsMostBlocks = 1u << 23;  // of a launch: a grid has less than 2^32 threads
 constexpr int kHeadPerLane = 16;  // elements of a head that a thread holds
 
-// Workgroups of the backward pass, at most: three on each CU, as its registers
-// allow for; each leaves a partial row of both weights' gradients.
+// Workgroups of the backward pass, at most; each leaves a partial row of both weights'
+// gradients.  Three on each CU, which the forms of bfloat16 vectors of 16 bytes reach
+// (146 to 154 registers).  The others have 172 to 234 and two on a CU, for which the
+// most is a round and a half (float32, 16384 x (16 + 4) heads of 128: 97 us, 5.2 TB/s).
 constexpr int kHeadBackBlocks = 768;
 inline int head_back_blocks(int ranks) { return kHeadBackBlocks / ranks; }
 

@@ -30,8 +30,8 @@ constexpr int back_waves()
 // side's weight (the other side's wait in LDS).  A workgroup's partial rows are
 // added to the others' by k_heads_dw_join, in a fixed order.
 //
-// Bound by memory: 16384 x (16 + 4) bfloat16 heads of 256 move their 503 MB in 114
-// us (4.4 TB/s), 8 ranks' 2048 x (8 + 2) of 128 their 126 MB in 32.
+// Bound by memory: 16384 x (16 + 4) bfloat16 heads of 256 move their 503 MB in 110
+// us (4.6 TB/s), 8 ranks' 2048 x (8 + 2) of 128 their 126 MB in 34.
 template <class E, int W, int LAYOUT, bool WHOLE>
 __global__ __launch_bounds__(kThreads, (back_waves<E, W>())) void k_heads_back(HeadsBackArgs a)
 {
