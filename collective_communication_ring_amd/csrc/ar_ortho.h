@@ -78,6 +78,7 @@ struct OrthoProductArgs {
                                 //   written to both its places
     float s_acc, s_add, diag;
     OrthoLift lift;
+    int ends;                   // a power of two that the last product's result gets besides
     const int* down;            // t of the first matrix, each / 2 ahead of the next one's
     // the last product: C goes to the caller's arrays instead, [m][n] or transposed
     int last, transposed, bf16;
@@ -115,6 +116,7 @@ struct OrthoSmallArgs {
     uint32_t rows, cols;
     int bf16, steps;
     float eps;
+    int ends;   // a power of two that the result gets besides
     double up;  // 2^e of the first X
     // a step's factors: A's, those of A A and A in B, of B X and X in X
     struct {

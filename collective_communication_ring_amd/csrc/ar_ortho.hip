@@ -63,6 +63,10 @@ __device__ inline int down_of(double norm)
 
 __device__ inline int above(int v) { return v > 0 ? v : 0; }
 
+// How much of a last product's power of two its result gets in the end: half of a
+// large one, as a factor that is subnormal has fewer bits.
+__device__ inline int halved_end(int power) { return power < -32 ? power / 2 : 0; }
+
 __device__ inline void split(float v, _Float16* hi, _Float16* lo)
 {
     *hi = (_Float16)v;
@@ -537,12 +541,14 @@ __global__ __launch_bounds__(64 * (B / WM) * (B / WN)) void k_ortho_product(Orth
     // product: four consecutive values of a row of C^T, and, after four lanes
     // exchanged theirs, of a row of C
     const uint32_t mp = padded(a.m), np = padded(a.n);
-    float s_acc = a.s_acc, s_add = a.s_add;
-    if (down) {
+    float s_acc = a.s_acc, s_add = a.s_add, s_out = 1.0f;
+    if (down || a.ends) {
         const OrthoLift& l = a.lift;
         const int now = above(down - l.now), next = above(down - l.next), b = above(2 * now - l.b);
-        s_acc = ldexpf(s_acc, l.acc[0] * now + l.acc[1] * next + l.acc[2] * b);
-        s_add = ldexpf(s_add, l.add[0] * now + l.add[1] * next + l.add[2] * b);
+        const int out = a.last ? halved_end(a.ends + next - now) : 0;
+        s_acc = ldexpf(s_acc, l.acc[0] * now + l.acc[1] * next + l.acc[2] * b + a.ends - out);
+        s_add = ldexpf(s_add, l.add[0] * now + l.add[1] * next + l.add[2] * b + a.ends - out);
+        s_out = ldexpf(1.0f, out);
     }
     const _Float16* dt = a.dt ? a.dt + own : nullptr;
     _Float16 *c = a.c + own, *ct = a.ct + own;
@@ -568,7 +574,7 @@ __global__ __launch_bounds__(64 * (B / WM) * (B / WN)) void k_ortho_product(Orth
                     if (dt)
                         v[r] = fmaf((float)dh[r] + (float)dl[r], s_add, v[r]);
                     v[r] += i + r == j ? a.diag : 0.0f;
-                    v[r] = i + r < a.m && j < a.n ? v[r] : 0.0f;
+                    v[r] = i + r < a.m && j < a.n ? v[r] * s_out : 0.0f;
                 }
                 uint32_t w[4];
                 if (a.last) {
@@ -758,15 +764,19 @@ __global__ __launch_bounds__(kSmallThreads) void k_ortho_small(OrthoPointers in,
             f(g, i0 + 8 * g.value + 4 * (lane / 32), j0 + lane % 32);
         });
     };
+    float s_out = 1.0f;
     for (int step = 0;; ++step) {
         auto k = a.step[step];
-        if (down) {  // as OrthoLift of the products
+        if (down || a.ends) {  // as the products' factors
+            const bool last = step + 1 == a.steps;
             const int now = above(down - a.lift[step]), next = above(down - a.lift[step + 1]);
-            const int b = above(2 * now - a.lift_b[step]);
+            const int b = above(2 * now - a.lift_b[step]), ends = last ? a.ends : 0;
+            const int out = last ? halved_end(ends + next - now) : 0;
             k.b_acc = ldexpf(k.b_acc, b - 4 * now);
             k.b_add = ldexpf(k.b_add, b - 2 * now);
-            k.x_acc = ldexpf(k.x_acc, next - now - b);
-            k.x_add = ldexpf(k.x_add, next - now);
+            k.x_acc = ldexpf(k.x_acc, next - now - b + ends - out);
+            k.x_add = ldexpf(k.x_add, next - now + ends - out);
+            s_out = ldexpf(1.0f, out);
         }
         if (has_a) {  // A = X X^T; A is its own transpose
             acc = small_tile(x, mp, ai, x, mp, aj, np, lane);
@@ -834,7 +844,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_ortho_small(OrthoPointers in,
             uint32_t w[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                u[r] = acc[4 * g.value + r];
+                u[r] = acc[4 * g.value + r] * s_out;
                 w[r] = __float_as_uint(u[r]);
             }
             if (tall) {

@@ -286,6 +286,9 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
     ex[p.steps] = 0;
     down[p.steps] = kOrthoGround;
 
+    // a small scale's power of two is the result's, not the last product's factors'
+    const int ends = p.scale != 0.0f && std::ilogb(p.scale) < -32 ? std::ilogb(p.scale) : 0;
+    const double own_scale = std::ldexp((double)p.scale, -ends);
     // what a step's sums and addends are multiplied by: coefficients, exponents, and
     // in the end the scale
     struct Factors {
@@ -293,7 +296,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
     };
     const auto factors = [&](int i) {
         const float* k = p.coefficients + 3 * i;
-        const double up = std::ldexp(i + 1 == p.steps ? (double)p.scale : 1.0, ex[i + 1] - ex[i]);
+        const double up = std::ldexp(i + 1 == p.steps ? own_scale : 1.0, ex[i + 1] - ex[i]);
         return Factors{(float)std::ldexp(1.0, ea[i] - 2 * ex[i]),
                        (float)std::ldexp((double)k[2], eb[i] - 2 * ea[i]),
                        (float)std::ldexp((double)k[1], eb[i] - ea[i]), (float)std::ldexp(up, -eb[i]),
@@ -319,6 +322,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             a.bf16 = p.dtype == AR_BF16;
             a.steps = p.steps;
             a.eps = p.eps;
+            a.ends = ends;
             a.up = std::ldexp(1.0, ex[0]);
             for (int i = 0; i < p.steps; ++i) {
                 const Factors f = factors(i);
@@ -389,7 +393,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             }
             const int end = i + group;
             const bool last = end == p.steps;
-            const double scale = last ? (double)p.scale : 1.0;
+            const double scale = last ? own_scale : 1.0;
             const _Float16 *x = w + l.x[now], *xt = w + l.xt[now];
             square(x, x, nullptr, A, long_k, std::ldexp(1.0, ea[i] - 2 * ex[i]), 0.0, 0.0, {});
             // the last product's factor of X: B, beside a X, or the group's polynomial F
@@ -443,6 +447,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             c.n = l.n;
             c.k = short_k;
             c.last = last;
+            c.ends = last ? ends : 0;
             if (group == 1) {  // X = a X + B X
                 const Factors f = factors(i);
                 c.dt = xt;
