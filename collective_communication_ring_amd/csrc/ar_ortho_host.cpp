@@ -385,7 +385,7 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
             int group = 1;
             for (double wide = 1.0; l.merged && group < kMergeMost && i + group < p.steps; ++group) {
                 // what the group's later steps take for A is off by that much more: 2^-23
-                // widened by 256 is a part in 64 of bfloat16's own rounding (4096 x 8192: 4.88
+                // widened by 256 is a part in 128 of bfloat16's own rounding (4096 x 8192: 4.88
                 // ms, by 16 5.33, 1.660e-3 off the 64-bit result either way)
                 wide *= widening(k + 3 * (group - 1), tops[i + group - 1]);
                 if (!(wide <= (p.dtype == AR_BF16 ? 256.0 : 16.0)))

@@ -670,7 +670,7 @@ size_t ar_head_rmsnorm_backward_workspace(int ranks, size_t dim); /* 0 for sizes
  * Steps of a large matrix much longer one way than the other may be taken up to
  * three together, X multiplied once by the product of their polynomials in A,
  * while that widens A's roundings by at most 16 (bfloat16, which rounds the
- * result to 2^-9: 256, a part of 2^-15).
+ * result to 2^-8: 256, a part of 2^-15).
  * The order of sums depends on sizes, the number of matrices and the workspace's
  * size alone.
  * A matrix of zeros gives zeros (eps > 0); one with an infinity or NaN gives
