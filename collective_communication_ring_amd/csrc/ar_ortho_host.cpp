@@ -286,8 +286,9 @@ extern "C" int ar_orthogonalize(const ar_orthogonalize_t* args, void* stream)
     ex[p.steps] = 0;
     down[p.steps] = kOrthoGround;
 
-    // a small scale's power of two is the result's, not the last product's factors'
-    const int ends = p.scale != 0.0f && std::ilogb(p.scale) < -32 ? std::ilogb(p.scale) : 0;
+    // a small result's power of two is its own, not the last product's factors'
+    const double result = std::fabs((double)p.scale) * top;
+    const int ends = power(result) < -32 ? power(result) : 0;
     const double own_scale = std::ldexp((double)p.scale, -ends);
     // what a step's sums and addends are multiplied by: coefficients, exponents, and
     // in the end the scale

@@ -52,3 +52,31 @@ def test_small_results(m, n, norm, eps, scale):
         torch.cuda.synchronize()
         off, size = float((y.cpu().double() - want).norm()), float(want.norm())
         assert off <= 1.01 * (lost + half) * size + least * (m * n) ** 0.5, (z.dtype, off, size)
+
+
+@pytest.mark.parametrize("m,n", [(40, 60), (130, 200)])
+@pytest.mark.parametrize("small", (1e-30, 1e-33, 1e-36))
+@pytest.mark.parametrize("scale", (1.0, 1e10, 1e-4))
+def test_small_coefficients(m, n, small, scale):
+    """The last step's coefficients make the result small.  It is at least half of |a|
+    |X| here (0.9 and more), so the bound above, divided by 1.9 and doubled, is one
+    relative to the result."""
+    import torch
+    from collective_communication_ring_amd import api
+    x = torch.randn((m, n), generator=torch.Generator().manual_seed(m))
+    k = [float(torch.tensor(v * small)) for v in K]
+    y = torch.empty((m, n), device="cuda")
+    for ks in ([k], [list(K), k]):
+        want = x.double() / (x.double().norm() + 1e-7)
+        for a, b, c in ks:
+            A = want @ want.t()
+            want = a * want + (b * A + c * A @ A) @ want
+        want = want * float(torch.tensor(scale))
+        api.orthogonalize(x.cuda(), y, len(ks), ks, 1e-7, scale)
+        torch.cuda.synchronize()
+        s, l = 2.0 ** -22 + 2.0 ** -24, lambda k: 2.0 ** -22 + 3 * k * 2.0 ** -23  # noqa: E731
+        dA = 3 * s + l(n)
+        dB = 1.4 * dA + 0.5 * (2 * dA + l(m)) + 2 * s
+        lost = 2.9 * (1.9 * s + dB + 2 * s + l(m)) / 1.9 * 2
+        off, size = float((y.cpu().double() - want).norm()), float(want.norm())
+        assert off <= 1.01 * lost * size + 2.0 ** -150 * (m * n) ** 0.5, (ks, off / size, lost)
